@@ -49,7 +49,8 @@ typedef enum {
 
 typedef enum { GPTQ_GRID_ASYM_MINMAX = 0, GPTQ_GRID_TERNARY = 1, GPTQ_GRID_SYM_MINMAX = 2 } gptq_grid_t;
 
-typedef enum { GPTQ_F16 = 0, GPTQ_F32 = 1, GPTQ_F64 = 2 } gptq_dtype_t;
+/* GPTQ_BF16: the key-value cache's calls only. */
+typedef enum { GPTQ_F16 = 0, GPTQ_F32 = 1, GPTQ_F64 = 2, GPTQ_BF16 = 3 } gptq_dtype_t;
 
 /* Which factor of the damped Hessian H_d the quantizer is given. */
 typedef enum {
@@ -319,6 +320,141 @@ gptq_status_t gptq_pack_codes(const uint8_t* codes, int64_t m, int64_t d, int32_
                               uint32_t* out, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * The paged key-value cache: what a generating block needs between its packed
+ * products (gptq_dequant_gemv). Not a step of the pages' method; the OPT
+ * decoder block (causal multi-head attention between q, k, v and out) is the
+ * one sequential calibration runs.
+ *
+ * gptq_kv_cache_t (host struct): the pages.
+ *  k, v     device, [n_pages][n_kv_heads][page_size][head_dim], 16-byte aligned;
+ *           consecutive pages page_stride elements apart (page_stride % 8 == 0,
+ *           at least n_kv_heads * page_size * head_dim; k and v may be
+ *           interleaved in one allocation), the rest contiguous.
+ *  dtype    GPTQ_F16 or GPTQ_BF16, also of q, out and the new rows.
+ *  page_size a power of two from 8 to 4096 (slots).
+ *  head_dim a multiple of 8 from 8 to 128.
+ * gptq_kv_seqs_t (host struct): the sequences that use them.
+ *  page_table device int32 [n_seqs][ld_table]: slot t of sequence b is row
+ *           t % page_size of page page_table[b][t / page_size]. Only the first
+ *           max_pages entries of a row are used (max_pages <= ld_table,
+ *           max_pages * page_size < 2^30); entries behind a sequence's length
+ *           are not read. A page may serve several sequences (a shared prefix)
+ *           as long as no call writes to it.
+ *  lens     device int32 [n_seqs]: slots in use, the call's new tokens counted.
+ *           Negative reads as 0, more than max_pages * page_size as that.
+ * An entry outside [0, n_pages) holds no slots: attention passes over them (they
+ * are in no softmax and get no weight), append and evict skip their rows. So
+ * whatever the table holds, no access leaves the buffers.
+ * Lengths, tables and offsets are read on the device when the kernels run: a
+ * captured graph replays with the values they hold then. */
+typedef struct {
+  void* k;
+  void* v;
+  int32_t dtype;
+  int32_t page_size;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int64_t n_pages;
+  int64_t page_stride;
+} gptq_kv_cache_t;
+
+typedef struct {
+  const int32_t* page_table;
+  int64_t ld_table;
+  int64_t max_pages;
+  const int32_t* lens;
+  int64_t n_seqs;
+} gptq_kv_seqs_t;
+
+/* Puts new keys and values into the pages: row i of k_new / v_new, new token j
+ * of n_b of sequence b, goes to slot lens[b] - n_b + j of every kv head.
+ *  k_new, v_new device [n_tokens][n_kv_heads][head_dim], tokens ldk / ldv
+ *           elements apart (% 8 == 0), 16-byte aligned; not in the cache.
+ *  cu_seqlens device int32 [n_seqs + 1]: sequence b's rows are cu_seqlens[b] ..
+ *           cu_seqlens[b + 1] - 1, ascending from 0; rows behind the last
+ *           sequence are not read. NULL: one row per sequence (n_tokens ==
+ *           n_seqs). A sequence may have none.
+ * Slots below 0 or beyond the table are skipped. Two sequences whose new slots
+ * share a page row leave one of the two there. */
+gptq_status_t gptq_kv_append(const gptq_kv_cache_t* cache, const gptq_kv_seqs_t* seqs, const void* k_new, int64_t ldk,
+                             const void* v_new, int64_t ldv, const int32_t* cu_seqlens, int64_t n_tokens,
+                             void* stream);
+
+/* Bytes of workspace of the attention calls (0 = none). n_tokens: 0 for
+ * gptq_paged_attention, the rows of q for gptq_paged_prefill; weights: whether
+ * weights are accumulated. 0 too for arguments that the calls refuse. */
+size_t gptq_kv_workspace_bytes(const gptq_kv_cache_t* cache, const gptq_kv_seqs_t* seqs, int64_t n_heads,
+                               int64_t window, int64_t sinks, int64_t n_tokens, int32_t weights);
+
+/* Attention of one new token per sequence, at position p = lens[b] - 1 (its key
+ * and value already in the cache): for query head h of group g = h / (n_heads /
+ * n_kv_heads), over the slots t <= p with window == 0, t > p - window or
+ * t < sinks, w_t = softmax_t(scale q_h . k_g[t]) and out_h = sum_t w_t v_g[t]. A
+ * sequence that sees nothing (length 0) gives zeros.
+ *  q        device [n_seqs][n_heads][head_dim], sequences ldq elements apart
+ *           (% 8 == 0), 16-byte aligned.  out: the same with ldo; may be q.
+ *  n_heads  a multiple of n_kv_heads, at most 1024 per kv head.
+ *  scale    finite (1 / sqrt(head_dim) in OPT).
+ *  window   0: every slot; else the last `window` slots. sinks >= 0: first slots
+ *           that stay visible with a window (no effect without one).
+ *  weights  device float [n_seqs][n_kv_heads][ldw] or NULL, ldw >= max_pages *
+ *           page_size: weights[b][g][t] += sum of w_t over the heads of group g;
+ *           entries of slots that are not seen stay as they are.
+ *  workspace 256-byte aligned, gptq_kv_workspace_bytes(...) bytes; written
+ *           before it is read, so it needs no clearing. Calls that may overlap
+ *           (other streams, two graphs) each need their own.
+ * Scores, maximum and sums are fp32; the weights enter the second product in the
+ * cache's type (bf16 in two terms). The result does not depend on the other
+ * sequences' lengths or on timing. */
+gptq_status_t gptq_paged_attention(const gptq_kv_cache_t* cache, const gptq_kv_seqs_t* seqs, const void* q,
+                                   int64_t ldq, int64_t n_heads, float scale, int64_t window, int64_t sinks,
+                                   float* weights, int64_t ldw, void* out, int64_t ldo, void* workspace,
+                                   size_t ws_bytes, void* stream);
+
+/* gptq_paged_attention for prompts, or the next chunks of longer ones: row j of
+ * the n_b = cu_seqlens[b + 1] - cu_seqlens[b] rows of sequence b stands at
+ * position p = lens[b] - n_b + j (causal; a row at a negative position sees
+ * nothing).
+ *  q, out   device [n_tokens][n_heads][head_dim], rows ldq / ldo elements apart.
+ *           Rows behind the last sequence (cu_seqlens[n_seqs] ..) are neither
+ *           read nor written. out may not overlap q.
+ *  cu_seqlens device int32 [n_seqs + 1], ascending from 0; a sequence whose
+ *           bounds leave [0, n_tokens] is passed over. n_tokens < 2^30.
+ *  weights  += the sum of w_t over the sequence's rows and the heads of a group.
+ * The weights enter the second product in the cache's type. */
+gptq_status_t gptq_paged_prefill(const gptq_kv_cache_t* cache, const gptq_kv_seqs_t* seqs, const void* q, int64_t ldq,
+                                 const int32_t* cu_seqlens, int64_t n_tokens, int64_t n_heads, float scale,
+                                 int64_t window, int64_t sinks, float* weights, int64_t ldw, void* out, int64_t ldo,
+                                 void* workspace, size_t ws_bytes, void* stream);
+
+/* Eviction by accumulated weight. Every sequence with n = lens[b] > budget slots
+ * keeps, per kv head, its first `sinks` and last `recent` slots and the
+ * budget - sinks - recent others with the largest weights (equal weights: the
+ * lower slot; -0 = +0; a NaN counts as larger than any number). The survivors
+ * keep their order and move to rows 0 .. budget - 1 of the sequence's new pages.
+ * Heads keep different slots, so afterwards a slot number is an order, no longer
+ * a position (OPT's positions are in its embeddings; windows count slots).
+ * Sequences with n <= budget stay where they are.
+ *  weights  device float [n_seqs][n_kv_heads][ldw], ldw >= max_pages * page_size
+ *           (as the attention calls accumulate them).
+ *  budget >= 1; sinks, recent >= 0; sinks + recent <= budget < 2^30.
+ *  new_pages device int32 [n_seqs][ld_new], ld_new >= ceil(budget / page_size):
+ *           free pages, used only by the sequences that lose slots; distinct
+ *           from one another and from every page in use.
+ *  table_out device int32 [n_seqs][ld_out], ld_out >= max_pages: the new row of a
+ *           sequence that lost slots (its new pages, then -1), the old row of
+ *           another. lens_out int32 [n_seqs]: min(n, budget).
+ *  weights_out device float [n_seqs][n_kv_heads][ldw_out], ldw_out >= max_pages *
+ *           page_size: the survivors' weights in their new order, 0 behind them.
+ *  kept     device int32 [n_seqs][n_kv_heads][budget]: the old slot of every new
+ *           one, -1 behind the last.
+ * No output may be an input (the pages excepted). Needs no workspace. */
+gptq_status_t gptq_kv_evict(const gptq_kv_cache_t* cache, const gptq_kv_seqs_t* seqs, const float* weights,
+                            int64_t ldw, int64_t budget, int64_t sinks, int64_t recent, const int32_t* new_pages,
+                            int64_t ld_new, int32_t* table_out, int64_t ld_out, int32_t* lens_out, float* weights_out,
+                            int64_t ldw_out, int32_t* kept, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Tracing (instrumentation, not a step of the method): device time per kernel
  * family. While a trace is active on the calling host thread, every kernel the
  * library launches from that thread is bracketed by two HIP events recorded on
@@ -336,7 +472,8 @@ enum {
   GPTQ_TRACE_SYRK = 0, GPTQ_TRACE_SYRK_REDUCE = 1, GPTQ_TRACE_CHAIN_LOAD = 2, GPTQ_TRACE_CHAIN_PANEL = 3,
   GPTQ_TRACE_CHAIN_UPDATE = 4, GPTQ_TRACE_CHAIN_MERGE = 5, GPTQ_TRACE_CHAIN_STORE = 6, GPTQ_TRACE_QUANT_PREP = 7,
   GPTQ_TRACE_COLLOOP = 8, GPTQ_TRACE_ESPLIT = 9, GPTQ_TRACE_TGEMM = 10, GPTQ_TRACE_PACK = 11,
-  GPTQ_TRACE_ORDER = 12, GPTQ_TRACE_GEMV = 13, GPTQ_TRACE_SYRK_TRANSPOSE = 14, GPTQ_TRACE_FAMILIES = 15
+  GPTQ_TRACE_ORDER = 12, GPTQ_TRACE_GEMV = 13, GPTQ_TRACE_SYRK_TRANSPOSE = 14, GPTQ_TRACE_KV_APPEND = 15,
+  GPTQ_TRACE_KV_ATTENTION = 16, GPTQ_TRACE_KV_EVICT = 17, GPTQ_TRACE_FAMILIES = 18
 };
 int32_t gptq_trace_start(void);
 int32_t gptq_trace_stop(int64_t* launches, double* ms, double* work, int32_t n);

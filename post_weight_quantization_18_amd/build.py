@@ -25,6 +25,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgptq_mi355x.so")
 LIB_DEBUG = os.path.join(PKG, "libgptq_mi355x_debug.so")
 SOURCES = ["gptq_api.hip", "syrk.hip", "chain.hip", "quant.hip", "trail.hip", "order.hip", "gemv.hip", "trace.hip",
+           "kv_cache.hip", "kv_token.hip", "kv_prompt.hip",
            "colloop_row.hip", "colloop_g16.hip", "colloop_g32.hip", "colloop_g64.hip", "colloop_g128.hip", "colloop_wide.hip",
            "colloop_static.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

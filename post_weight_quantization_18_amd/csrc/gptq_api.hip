@@ -6,6 +6,7 @@
 #include <new>
 
 #include "common.h"
+#include "kv.h"
 
 namespace gptq {
 size_t quant_workspace_bytes_u64(int64_t m, int64_t d, const gptq_qcfg_t& cfg);
@@ -72,6 +73,61 @@ gptq_qcfg_t default_qcfg() {
 }
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+// The cache and its sequences as the kernels take them, or why not.
+gptq_status_t kv_view(const gptq_kv_cache_t* c, const gptq_kv_seqs_t* s, KvView* out) {
+  if (!c || !s || !c->k || !c->v || !s->page_table || !s->lens) return GPTQ_ERR_INVALID_ARG;
+  if (c->dtype != GPTQ_F16 && c->dtype != GPTQ_BF16) return GPTQ_ERR_INVALID_ARG;
+  if (c->page_size < 8 || c->page_size > 4096 || (c->page_size & (c->page_size - 1))) return GPTQ_ERR_UNSUPPORTED;
+  if (c->head_dim <= 0 || c->n_kv_heads <= 0 || c->n_pages <= 0 || s->n_seqs <= 0) return GPTQ_ERR_INVALID_ARG;
+  if (c->head_dim % 8 || c->head_dim > 128) return GPTQ_ERR_UNSUPPORTED;
+  if (c->n_kv_heads > 65536 || s->n_seqs > ((int64_t)1 << 24) || c->n_pages > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
+  const int64_t page = (int64_t)c->n_kv_heads * c->page_size * c->head_dim;
+  if (c->page_stride < page || c->page_stride % 8 || !aligned(c->k, 16) || !aligned(c->v, 16)) return GPTQ_ERR_INVALID_ARG;
+  if (s->max_pages <= 0 || s->ld_table < s->max_pages) return GPTQ_ERR_INVALID_ARG;
+  if (s->max_pages >= ((int64_t)1 << 30) / c->page_size) return GPTQ_ERR_UNSUPPORTED;
+  KvView v{};
+  v.k = c->k;
+  v.v = c->v;
+  v.table = s->page_table;
+  v.lens = s->lens;
+  v.page_stride = c->page_stride;
+  v.ld_table = s->ld_table;
+  v.n_pages = c->n_pages;
+  v.n_seqs = (int32_t)s->n_seqs;
+  v.n_kv = c->n_kv_heads;
+  v.dim = c->head_dim;
+  v.page_size = c->page_size;
+  v.page_shift = __builtin_ctz((unsigned)c->page_size);
+  v.max_pages = (int32_t)s->max_pages;
+  v.bf16 = c->dtype == GPTQ_BF16;
+  *out = v;
+  return GPTQ_OK;
+}
+
+// The arguments both attention calls share.
+gptq_status_t kv_attn_args(const KvView& c, const void* q, int64_t ldq, int64_t n_heads, float scale, int64_t window,
+                           int64_t sinks, float* weights, int64_t ldw, void* out, int64_t ldo, KvAttnArgs* r) {
+  const int64_t cap = (int64_t)c.max_pages * c.page_size;
+  if (!q || !out || n_heads <= 0 || n_heads % c.n_kv) return GPTQ_ERR_INVALID_ARG;
+  if (n_heads / c.n_kv > 1024) return GPTQ_ERR_UNSUPPORTED;
+  if (ldq % 8 || ldo % 8 || ldq < n_heads * c.dim || ldo < n_heads * c.dim) return GPTQ_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16)) return GPTQ_ERR_INVALID_ARG;
+  if (!(scale - scale == 0.0f) || window < 0 || sinks < 0) return GPTQ_ERR_INVALID_ARG;
+  if (weights && (ldw < cap || !aligned(weights, 4))) return GPTQ_ERR_INVALID_ARG;
+  r->q = q;
+  r->ldq = ldq;
+  r->out = out;
+  r->ldo = ldo;
+  r->weights = weights;
+  r->ldw = ldw;
+  r->scale = scale;
+  r->n_heads = (int32_t)n_heads;
+  // a window of the whole capacity hides nothing; more sinks than slots are all of them
+  r->window = window < cap ? (int32_t)window : 0;
+  r->sinks = (int32_t)(sinks < cap ? sinks : cap);
+  return GPTQ_OK;
+}
 
 }  // namespace
 
@@ -254,6 +310,94 @@ gptq_status_t gptq_pack_codes(const uint8_t* codes, int64_t m, int64_t d, int32_
   if ((d * bits) % 32) return GPTQ_ERR_INVALID_ARG;
   GPTQ_CHECK_DEVICE();
   return pack_enqueue(codes, d, m, d, bits, out, (hipStream_t)stream);
+}
+
+gptq_status_t gptq_kv_append(const gptq_kv_cache_t* cache, const gptq_kv_seqs_t* seqs, const void* k_new, int64_t ldk,
+                             const void* v_new, int64_t ldv, const int32_t* cu_seqlens, int64_t n_tokens,
+                             void* stream) {
+  KvView c;
+  if (const gptq_status_t s = kv_view(cache, seqs, &c)) return s;
+  const int64_t row = (int64_t)c.n_kv * c.dim;
+  if (n_tokens < 0 || n_tokens >= ((int64_t)1 << 30) || (!cu_seqlens && n_tokens != c.n_seqs)) return GPTQ_ERR_INVALID_ARG;
+  if (n_tokens == 0) return GPTQ_OK;
+  if (!k_new || !v_new || ldk < row || ldv < row || ldk % 8 || ldv % 8) return GPTQ_ERR_INVALID_ARG;
+  if (!aligned(k_new, 16) || !aligned(v_new, 16)) return GPTQ_ERR_INVALID_ARG;
+  GPTQ_CHECK_DEVICE();
+  return kv_append_enqueue(c, k_new, ldk, v_new, ldv, cu_seqlens, n_tokens, (hipStream_t)stream);
+}
+
+size_t gptq_kv_workspace_bytes(const gptq_kv_cache_t* cache, const gptq_kv_seqs_t* seqs, int64_t n_heads,
+                               int64_t window, int64_t sinks, int64_t n_tokens, int32_t weights) {
+  KvView c;
+  if (kv_view(cache, seqs, &c) || n_heads <= 0 || n_heads % c.n_kv || n_heads / c.n_kv > 1024) return 0;
+  if (window < 0 || sinks < 0 || n_tokens < 0 || n_tokens >= ((int64_t)1 << 30)) return 0;
+  if (n_tokens > 0) return kv_prompt_workspace_bytes(n_tokens, n_heads, weights != 0);
+  return kv_token_workspace_bytes(c, n_heads, window, sinks, weights != 0);
+}
+
+gptq_status_t gptq_paged_attention(const gptq_kv_cache_t* cache, const gptq_kv_seqs_t* seqs, const void* q,
+                                   int64_t ldq, int64_t n_heads, float scale, int64_t window, int64_t sinks,
+                                   float* weights, int64_t ldw, void* out, int64_t ldo, void* workspace,
+                                   size_t ws_bytes, void* stream) {
+  KvView c;
+  KvAttnArgs a;
+  if (const gptq_status_t s = kv_view(cache, seqs, &c)) return s;
+  if (const gptq_status_t s = kv_attn_args(c, q, ldq, n_heads, scale, window, sinks, weights, ldw, out, ldo, &a))
+    return s;
+  const size_t need = kv_token_workspace_bytes(c, n_heads, a.window, a.sinks, weights != nullptr);
+  if (need && (!workspace || ws_bytes < need || !aligned(workspace, 256))) return GPTQ_ERR_WORKSPACE;
+  GPTQ_CHECK_DEVICE();
+  return kv_token_enqueue(c, a, workspace, (hipStream_t)stream);
+}
+
+gptq_status_t gptq_paged_prefill(const gptq_kv_cache_t* cache, const gptq_kv_seqs_t* seqs, const void* q, int64_t ldq,
+                                 const int32_t* cu_seqlens, int64_t n_tokens, int64_t n_heads, float scale,
+                                 int64_t window, int64_t sinks, float* weights, int64_t ldw, void* out, int64_t ldo,
+                                 void* workspace, size_t ws_bytes, void* stream) {
+  KvView c;
+  KvAttnArgs a;
+  if (const gptq_status_t s = kv_view(cache, seqs, &c)) return s;
+  if (!cu_seqlens || n_tokens < 0 || n_tokens >= ((int64_t)1 << 30)) return GPTQ_ERR_INVALID_ARG;
+  if (n_tokens == 0) return GPTQ_OK;
+  if (const gptq_status_t s = kv_attn_args(c, q, ldq, n_heads, scale, window, sinks, weights, ldw, out, ldo, &a))
+    return s;
+  if (out == q) return GPTQ_ERR_INVALID_ARG;
+  const size_t need = kv_prompt_workspace_bytes(n_tokens, n_heads, weights != nullptr);
+  if (need && (!workspace || ws_bytes < need || !aligned(workspace, 256))) return GPTQ_ERR_WORKSPACE;
+  GPTQ_CHECK_DEVICE();
+  return kv_prompt_enqueue(c, a, cu_seqlens, n_tokens, workspace, (hipStream_t)stream);
+}
+
+gptq_status_t gptq_kv_evict(const gptq_kv_cache_t* cache, const gptq_kv_seqs_t* seqs, const float* weights,
+                            int64_t ldw, int64_t budget, int64_t sinks, int64_t recent, const int32_t* new_pages,
+                            int64_t ld_new, int32_t* table_out, int64_t ld_out, int32_t* lens_out, float* weights_out,
+                            int64_t ldw_out, int32_t* kept, void* stream) {
+  KvView c;
+  if (const gptq_status_t s = kv_view(cache, seqs, &c)) return s;
+  const int64_t cap = (int64_t)c.max_pages * c.page_size;
+  if (!weights || !new_pages || !table_out || !lens_out || !weights_out || !kept) return GPTQ_ERR_INVALID_ARG;
+  if (budget < 1 || sinks < 0 || recent < 0 || sinks > budget || recent > budget - sinks) return GPTQ_ERR_INVALID_ARG;
+  if (budget >= ((int64_t)1 << 30)) return GPTQ_ERR_UNSUPPORTED;
+  if (ldw < cap || ldw_out < cap || ld_out < c.max_pages || ld_new < ceil_div(budget, c.page_size))
+    return GPTQ_ERR_INVALID_ARG;
+  if (table_out == c.table || table_out == new_pages || lens_out == c.lens || weights_out == weights)
+    return GPTQ_ERR_INVALID_ARG;
+  GPTQ_CHECK_DEVICE();
+  KvEvictArgs a;
+  a.weights = weights;
+  a.ldw = ldw;
+  a.budget = (int32_t)budget;
+  a.sinks = (int32_t)sinks;
+  a.recent = (int32_t)recent;
+  a.dst = new_pages;
+  a.ld_dst = ld_new;
+  a.table_out = table_out;
+  a.ld_out = ld_out;
+  a.lens_out = lens_out;
+  a.weights_out = weights_out;
+  a.ldw_out = ldw_out;
+  a.kept = kept;
+  return kv_evict_enqueue(c, a, (hipStream_t)stream);
 }
 
 }  // extern "C"

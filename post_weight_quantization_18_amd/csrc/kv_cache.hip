@@ -1,0 +1,258 @@
+// What changes a paged key-value cache: new rows come in (append), and the rows
+// with the smallest accumulated attention weight leave (evict). Both move bytes
+// and compute next to nothing: they are bound by HBM, or by latency when small.
+#include "kv.h"
+
+namespace gptq {
+namespace {
+
+// Append. New token i of sequence b goes to slot lens[b] - n_b + (its index
+// among the n_b new ones). One thread per 16 bytes of a token's key or value
+// (grid.y covers a row's chunks), TOK tokens per block, all loads of a thread
+// before its stores. Slots or pages outside the table or the cache are skipped.
+template <int TOK>
+__global__ __launch_bounds__(256) void append_kernel(KvView c, const uint4v* k_new, int64_t ldk, const uint4v* v_new,
+                                                     int64_t ldv, const int32_t* cu, int n_tokens) {
+  const int per_head = c.dim >> 3, half = c.n_kv * per_head;
+  const int ch = blockIdx.y * 256 + threadIdx.x;
+  if (ch >= 2 * half) return;
+  const bool is_v = ch >= half;
+  const int rc = is_v ? ch - half : ch;
+  const int h = rc / per_head, off = (rc - h * per_head) * 8;
+  const uint4v* src = is_v ? v_new : k_new;
+  const int64_t ld = (is_v ? ldv : ldk) >> 3;
+  bf16_t* dst = (bf16_t*)(is_v ? c.v : c.k);  // 16-bit elements of either type
+  const int cap = c.max_pages << c.page_shift;
+  uint4v x[TOK];
+  int64_t to[TOK];
+#pragma unroll
+  for (int t = 0; t < TOK; ++t) {
+    to[t] = -1;
+    const int i = blockIdx.x * TOK + t;
+    int first = 0, last = n_tokens;
+    if (cu) {
+      first = cu[0];
+      last = cu[c.n_seqs];
+    }
+    if (i >= n_tokens || i < first || i >= last) continue;
+    const int b = cu ? kv_seq_of(cu, c.n_seqs, i) : i;
+    const int n_b = cu ? cu[b + 1] - cu[b] : 1, at = cu ? i - cu[b] : 0;
+    const int64_t slot = (int64_t)c.lens[b] - n_b + at;
+    if (slot < 0 || slot >= cap) continue;
+    const int page = c.table[(int64_t)b * c.ld_table + (slot >> c.page_shift)];
+    if (!c.page_ok(page)) continue;
+    to[t] = c.head_base(page, h) + (slot & (c.page_size - 1)) * c.dim + off;
+    x[t] = src[(int64_t)i * ld + rc];
+  }
+#pragma unroll
+  for (int t = 0; t < TOK; ++t)
+    if (to[t] >= 0) *(uint4v*)(dst + to[t]) = x[t];
+}
+
+// Order-preserving key of a sum: larger weight, larger key; a NaN above all, and
+// -0 as +0.
+__device__ __forceinline__ uint32_t weight_key(float w) {
+  if (w != w) return 0xffffffffu;
+  const uint32_t u = __builtin_bit_cast(uint32_t, w + 0.0f);
+  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+constexpr int kSelThreads = 1024, kSelWaves = kSelThreads / 64, kBins = 2048;
+
+// Select: for one sequence and head, the slots that stay, in order. With
+// n > budget slots, the first `sinks` and the last `recent` stay, and of those
+// between the need = budget - sinks - recent with the largest weights, ties to
+// the lower slot. The need-th largest key is found digit by digit (11, 11 and
+// 10 bits) from a histogram in LDS; then each wave counts its contiguous part of
+// the slots, the waves' counts are summed, and each writes its survivors.
+__global__ __launch_bounds__(kSelThreads) void evict_select_kernel(KvView c, KvEvictArgs a) {
+  __shared__ uint32_t hist[kBins];
+  __shared__ uint32_t wave_sum[kSelWaves], wave_eq[kSelWaves];
+  __shared__ uint32_t found_digit, found_left;
+  const int b = blockIdx.x / c.n_kv, h = blockIdx.x - b * c.n_kv;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int n = c.len(b);
+  int32_t* kept = a.kept + ((int64_t)b * c.n_kv + h) * a.budget;
+  if (n <= a.budget) {
+    for (int i = tid; i < a.budget; i += kSelThreads) kept[i] = i < n ? i : -1;
+    return;
+  }
+  const float* w = a.weights + ((int64_t)b * c.n_kv + h) * a.ldw;
+  const int lo = a.sinks, hi = n - a.recent;  // the slots that compete
+  const uint32_t need = a.budget - a.sinks - a.recent;
+  uint32_t prefix = 0, mask = 0, left = need;
+  if (need > 0) {
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+      for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+      __syncthreads();
+      for (int t = lo + tid; t < hi; t += kSelThreads) {
+        const uint32_t key = weight_key(w[t]);
+        if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1)], 1u);
+      }
+      __syncthreads();
+      // bins from the largest: thread i holds bins 2047 - 2 i and 2046 - 2 i
+      const uint32_t h0 = hist[kBins - 1 - 2 * tid], h1 = hist[kBins - 2 - 2 * tid];
+      uint32_t incl = h0 + h1;
+      for (int o = 1; o < 64; o <<= 1) {
+        const uint32_t u = __shfl_up(incl, o);
+        if (lane >= o) incl += u;
+      }
+      if (lane == 63) wave_sum[wave] = incl;
+      __syncthreads();
+      uint32_t before = incl - h0 - h1;
+      for (int k = 0; k < wave; ++k) before += wave_sum[k];
+      if (before < left && before + h0 >= left) {
+        found_digit = kBins - 1 - 2 * tid;
+        found_left = left - before;
+      } else if (before + h0 < left && before + h0 + h1 >= left) {
+        found_digit = kBins - 2 - 2 * tid;
+        found_left = left - before - h0;
+      }
+      __syncthreads();
+      prefix |= found_digit << shift;
+      mask |= ((1u << bits) - 1) << shift;
+      left = found_left;
+    }
+  }
+  // slots with key > prefix stay, and the first `left` with key == prefix
+  const int per_wave = ((n + 63) / 64 + kSelWaves - 1) / kSelWaves * 64;
+  const int t0 = wave * per_wave, t1 = t0 + per_wave < n ? t0 + per_wave : n;
+  uint32_t sure = 0, equal = 0;
+  for (int r = t0; r < t1; r += 64) {
+    const int t = r + lane;
+    bool s = false, e = false;
+    if (t < t1) {
+      s = t < lo || t >= hi;
+      if (!s && need > 0) {
+        const uint32_t key = weight_key(w[t]);
+        s = key > prefix;
+        e = key == prefix;
+      }
+    }
+    sure += __popcll(__ballot(s));
+    equal += __popcll(__ballot(e));
+  }
+  __syncthreads();  // wave_sum of the last pass has been read
+  if (lane == 0) {
+    wave_sum[wave] = sure;
+    wave_eq[wave] = equal;
+  }
+  __syncthreads();
+  uint32_t sure_before = 0, eq_before = 0;
+  for (int k = 0; k < wave; ++k) {
+    sure_before += wave_sum[k];
+    eq_before += wave_eq[k];
+  }
+  uint32_t base = sure_before + (eq_before < left ? eq_before : left);
+  const uint64_t below = lane == 0 ? 0ull : ~0ull >> (64 - lane);
+  for (int r = t0; r < t1; r += 64) {
+    const int t = r + lane;
+    bool s = false, e = false;
+    if (t < t1) {
+      s = t < lo || t >= hi;
+      if (!s && need > 0) {
+        const uint32_t key = weight_key(w[t]);
+        s = key > prefix;
+        e = key == prefix;
+      }
+    }
+    const uint64_t em = __ballot(e);
+    if (e && eq_before + __popcll(em & below) < left) s = true;
+    eq_before += __popcll(em);
+    const uint64_t sm = __ballot(s);
+    const uint32_t at = base + __popcll(sm & below);
+    if (s && at < (uint32_t)a.budget) kept[at] = t;
+    base += __popcll(sm);
+  }
+}
+
+// Move: the survivors' rows to the new pages, their sums to weights_out (zero
+// behind them), the table's row and the length. 16 lanes per row of up to 256
+// bytes, key and value together, kMoveRows rows per block, a thread's loads
+// before its stores. Source and destination pages are distinct, so every row
+// moves on its own.
+constexpr int kMoveRows = 64;
+
+__global__ __launch_bounds__(256) void evict_move_kernel(KvView c, KvEvictArgs a, int n_blk) {
+  const int blk = blockIdx.x % n_blk, bh = blockIdx.x / n_blk;
+  const int b = bh / c.n_kv, h = bh - b * c.n_kv;
+  const int tid = threadIdx.x;
+  const int n = c.len(b);
+  const bool over = n > a.budget;
+  const int cap = c.max_pages << c.page_shift, left = over ? a.budget : n;
+  const int32_t* kept = a.kept + ((int64_t)b * c.n_kv + h) * a.budget;
+  const int32_t* row = c.table + (int64_t)b * c.ld_table;
+  const int32_t* dst = a.dst + (int64_t)b * a.ld_dst;
+  const int r0 = blk * kMoveRows;
+  if (tid < kMoveRows && r0 + tid < cap) {
+    const int i = r0 + tid;
+    float s = 0.0f;
+    if (i < left) s = a.weights[((int64_t)b * c.n_kv + h) * a.ldw + (over ? kept[i] : i)];
+    a.weights_out[((int64_t)b * c.n_kv + h) * a.ldw_out + i] = s;
+  }
+  if (blk == 0 && h == 0) {
+    const int nd = (a.budget + c.page_size - 1) >> c.page_shift;
+    for (int p = tid; p < c.max_pages; p += 256)
+      a.table_out[(int64_t)b * a.ld_out + p] = !over ? row[p] : p < nd ? dst[p] : -1;
+    if (tid == 0) a.lens_out[b] = left;
+  }
+  if (!over) return;
+  const int ch = tid & 15;
+  if (ch * 8 >= c.dim) return;
+  constexpr int U = kMoveRows / 16;
+  uint4v xk[U], xv[U];
+  int64_t to[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    to[u] = -1;
+    const int i = r0 + u * 16 + (tid >> 4);
+    if (i >= a.budget) continue;
+    const int t = kept[i];
+    GPTQ_DASSERT(t >= 0 && t < n);
+    const int ps = row[t >> c.page_shift], pd = dst[i >> c.page_shift];
+    if (!c.page_ok(ps) || !c.page_ok(pd)) continue;
+    const int64_t from = c.head_base(ps, h) + (int64_t)(t & (c.page_size - 1)) * c.dim + ch * 8;
+    to[u] = c.head_base(pd, h) + (int64_t)(i & (c.page_size - 1)) * c.dim + ch * 8;
+    xk[u] = *(const uint4v*)((const bf16_t*)c.k + from);
+    xv[u] = *(const uint4v*)((const bf16_t*)c.v + from);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (to[u] < 0) continue;
+    *(uint4v*)((bf16_t*)c.k + to[u]) = xk[u];
+    *(uint4v*)((bf16_t*)c.v + to[u]) = xv[u];
+  }
+}
+
+}  // namespace
+
+gptq_status_t kv_append_enqueue(const KvView& c, const void* k_new, int64_t ldk, const void* v_new, int64_t ldv,
+                                const int32_t* cu, int64_t n_tokens, hipStream_t st) {
+  const unsigned gy = (unsigned)ceil_div(2 * (int64_t)c.n_kv * (c.dim >> 3), 256);
+  TraceScope tr(st, GPTQ_TRACE_KV_APPEND);
+  // four tokens per block once that still leaves a few blocks for every compute unit
+  if (n_tokens * gy >= 8192)
+    hipLaunchKernelGGL(append_kernel<4>, dim3((unsigned)ceil_div(n_tokens, 4), gy), dim3(256), 0, st, c,
+                       (const uint4v*)k_new, ldk, (const uint4v*)v_new, ldv, cu, (int)n_tokens);
+  else
+    hipLaunchKernelGGL(append_kernel<1>, dim3((unsigned)n_tokens, gy), dim3(256), 0, st, c, (const uint4v*)k_new, ldk,
+                       (const uint4v*)v_new, ldv, cu, (int)n_tokens);
+  GPTQ_CHECK_LAUNCH();
+  return GPTQ_OK;
+}
+
+gptq_status_t kv_evict_enqueue(const KvView& c, const KvEvictArgs& a, hipStream_t st) {
+  const int64_t cap = (int64_t)c.max_pages << c.page_shift;
+  // a budget beyond the capacity moves nothing: the blocks cover the capacity's sums
+  const int64_t n_blk = ceil_div(cap, kMoveRows), blocks = n_blk * c.n_kv * c.n_seqs;
+  if (blocks * 256 >= (int64_t)1 << 32) return GPTQ_ERR_UNSUPPORTED;
+  TraceScope tr(st, GPTQ_TRACE_KV_EVICT);
+  hipLaunchKernelGGL(evict_select_kernel, dim3((unsigned)(c.n_kv * c.n_seqs)), dim3(kSelThreads), 0, st, c, a);
+  GPTQ_CHECK_LAUNCH();
+  hipLaunchKernelGGL(evict_move_kernel, dim3((unsigned)blocks), dim3(256), 0, st, c, a, (int)n_blk);
+  GPTQ_CHECK_LAUNCH();
+  return GPTQ_OK;
+}
+
+}  // namespace gptq

@@ -1,0 +1,440 @@
+// Attention of one new token per sequence over the paged cache:
+//   s_t = scale q . k_t over the visible slots t, w = softmax(s), out = sum_t w_t v_t
+// and, if asked for, weights[t] += w_t summed over the heads that share a key.
+//
+// Every visible key and value is read once; with G heads to a key there are 2 G
+// flops per element read, so it is bound by HBM. The matrix cores take the
+// products all the same, because they cost less issue than vector code even
+// with one head to a key (15 of 16 columns idle): a wave's 32 slots x 128 are
+// 16 matrix instructions, 256 cycles for 16 KB, against a share of about 4 bytes
+// per cycle and SIMD of HBM bandwidth.
+//
+// One pass with a running maximum and sum. A wave takes 32 slots at a time, as
+// S^T = K Q^T (two 16 x 16 tiles) and O^T = V^T P^T, all in registers:
+//  - lane l = 16 g + c. K rows are assigned to the rows m of tile a as slot
+//    8 (m / 4) + 4 a + m % 4, so the scores a lane ends up with (rows 4 g + r)
+//    are slots 8 g .. 8 g + 7 of head c: exactly the P^T operand it must hold.
+//  - V rows 8 g .. 8 g + 7 are read along the row (elements c VEC ...), and an
+//    8 x VEC block is turned over inside each lane (32 byte permutes for 64
+//    elements), so no shared memory and no lane exchange lies in the loop.
+//  - the next 32 slots are loaded while the current ones are computed, and the
+//    page numbers one step further ahead.
+// The maximum is only raised when a score passes it by 2^8 (then every lane of
+// the wave rescales): weights stay below 2^8, well inside fp16, and the usual
+// step needs no exchange between lanes.
+//
+// The slots are split over the waves of a block and over n_splits blocks; a
+// block's waves are joined through LDS, the blocks by a second kernel (which also
+// turns the stored scores into weights).
+#include "kv.h"
+
+namespace gptq {
+namespace {
+
+constexpr int kTile = 32;     // slots per wave and step
+constexpr int kWaves = 4;     // waves per block
+constexpr float kRaise = 8.0f;  // in powers of two
+
+// The slots a token sees, as steps of kTile slots: the steps that hold sinks, then
+// those from the window's first slot on.
+struct Steps {
+  int n, first, sink_steps, total;  // slots, first slot of the window, steps before the gap, steps
+  int jump;                         // step number of the first step after the gap
+  __device__ __forceinline__ Steps(int len, int window, int sinks) {
+    n = len;
+    first = window > 0 && window < len ? len - window : 0;
+    const int all = (len + kTile - 1) / kTile;
+    const int sk = first > 0 ? (sinks < first ? sinks : first) : 0;
+    sink_steps = (sk + kTile - 1) / kTile;
+    jump = first / kTile;
+    if (jump < sink_steps) jump = sink_steps;
+    total = sink_steps + all - jump;
+  }
+  __device__ __forceinline__ int slot0(int s) const { return (s < sink_steps ? s : s - sink_steps + jump) * kTile; }
+};
+
+// Elements of the workspace (floats): per (sequence, head, split) the running
+// maximum, the sum and the unnormalized output; then the scores by step.
+struct TokenWs {
+  float* ml;      // [n_seqs * n_heads][n_splits][2]
+  float* o;       // [n_seqs * n_heads][n_splits][dim]
+  float* scores;  // [n_seqs * n_heads][n_scores]
+  int n_splits, n_scores;
+};
+
+template <typename T, int KS, int VEC>
+struct TokenRegs {
+  typename KvType<T>::x8 k[2][KS];
+  uint32_t v[8][VEC / 2];
+};
+
+// KS: steps of 32 along the head for the scores; VEC: output elements per lane
+// (16 VEC >= dim). SPLIT: partial results to the workspace. SCORES: they are
+// stored too.
+template <typename T, int KS, int VEC, bool SPLIT, bool SCORES>
+__global__ __launch_bounds__(64 * kWaves, 2) void token_kernel(KvView c, KvAttnArgs a, TokenWs w) {
+  using KT = KvType<T>;
+  using x8 = typename KT::x8;
+  const int lane = threadIdx.x & 63, g = lane >> 4, cl = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int group = a.n_heads / c.n_kv, qt = (group + 15) / 16;  // heads in tiles of 16
+  int id = blockIdx.x;
+  const int split = id % w.n_splits;
+  id /= w.n_splits;
+  const int h0 = (id % qt) * 16;
+  id /= qt;
+  const int kvh = id % c.n_kv, b = id / c.n_kv;
+  const int n_h = group - h0 < 16 ? group - h0 : 16;
+  const int head = kvh * group + h0 + (cl < n_h ? cl : 0);  // this lane's column
+
+  const Steps st(c.len(b), a.window, a.sinks);
+  const int per = (st.total + w.n_splits - 1) / w.n_splits;
+  const int s_end = (split + 1) * per < st.total ? (split + 1) * per : st.total;
+  const int32_t* table = c.table + (int64_t)b * c.ld_table;
+  const int chunks = c.dim >> 3;
+
+  x8 q[KS];
+  const T* qp = (const T*)a.q + (int64_t)b * a.ldq + (int64_t)head * c.dim;
+#pragma unroll
+  for (int i = 0; i < KS; ++i) {
+    const bool ok = 4 * i + g < chunks && cl < n_h;
+    x8 z = *(const x8*)(qp + 8 * (4 * i + g < chunks ? 4 * i + g : 0));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q[i][e] = ok ? z[e] : (T)0.0f;
+  }
+  const float sc = a.scale * kLog2e;
+
+  float4v o[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) o[i] = (float4v){0, 0, 0, 0};
+  float m = -INFINITY, lsum = 0.0f;  // of this lane's column; lsum over this lane's own slots
+
+  // page of the octet of 8 slots whose keys (o_k) or values (o_v) this lane loads, -1 if none
+  struct Pages {
+    int k, v;
+  };
+  auto pages = [&](int s) __attribute__((always_inline)) {
+    Pages p = {-1, -1};
+    if (s < s_end) {
+      const int t0 = st.slot0(s), tk = t0 + 8 * (cl >> 2), tv = t0 + 8 * g;
+      if (tk < st.n) p.k = table[tk >> c.page_shift];
+      if (tv < st.n) p.v = table[tv >> c.page_shift];
+    }
+    return p;
+  };
+  using Regs = TokenRegs<T, KS, VEC>;
+  const T* kbase = (const T*)c.k + (int64_t)kvh * c.page_size * c.dim;
+  const T* vbase = (const T*)c.v + (int64_t)kvh * c.page_size * c.dim;
+  const int vch = cl * VEC < c.dim ? cl * VEC : 0;
+  auto load = [&](int s, Pages p, Regs& r) __attribute__((always_inline)) {
+    const int t0 = st.slot0(s);
+    const int pk = c.page_ok(p.k) ? p.k : 0, pv = c.page_ok(p.v) ? p.v : 0;
+    const int rk = (t0 + 8 * (cl >> 2) + (cl & 3)) & (c.page_size - 1), rv = (t0 + 8 * g) & (c.page_size - 1);
+    const T* kp = kbase + (int64_t)pk * c.page_stride + rk * c.dim;
+    const T* vp = vbase + (int64_t)pv * c.page_stride + rv * c.dim + vch;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < KS; ++i)
+        r.k[t][i] = *(const x8*)(kp + 4 * t * c.dim + 8 * (4 * i + g < chunks ? 4 * i + g : 0));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if constexpr (VEC == 8) {
+        const uint4v x = *(const uint4v*)(vp + j * c.dim);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r.v[j][e] = x[e];
+      } else {
+        const uint2v x = *(const uint2v*)(vp + j * c.dim);
+        r.v[j][0] = x[0];
+        r.v[j][1] = x[1];
+      }
+    }
+  };
+  auto compute = [&](int s, Pages p, Regs& r) __attribute__((always_inline)) {
+    const int t0 = st.slot0(s);
+    // elements beyond the head in the last chunks: the row behind, not this one's
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+      if (KS > 2 && i < KS - 1) continue;
+      const bool ok = 4 * i + g < chunks;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const uint4v z = __builtin_bit_cast(uint4v, r.k[t][i]);
+        r.k[t][i] = __builtin_bit_cast(x8, (uint4v){ok ? z[0] : 0u, ok ? z[1] : 0u, ok ? z[2] : 0u, ok ? z[3] : 0u});
+      }
+    }
+    float x[8];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      float4v acc = {0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < KS; ++i) acc = KT::mfma16(r.k[t][i], q[i], acc);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[4 * t + e] = acc[e] * sc;
+    }
+    // slots past the end, before the window or on no page: out of the scores, and their
+    // values zeroed (0 x NaN is not 0)
+    const bool whole = t0 + kTile <= st.n && (t0 >= st.first || t0 + kTile <= a.sinks);
+    const bool vok = c.page_ok(p.v);
+    if (!whole || __any(!vok)) {
+      const int tv = t0 + 8 * g;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const bool ok = vok && tv + j < st.n && (tv + j >= st.first || tv + j < a.sinks);
+        x[j] = ok ? x[j] : -INFINITY;
+#pragma unroll
+        for (int e = 0; e < VEC / 2; ++e) r.v[j][e] = ok ? r.v[j][e] : 0u;
+      }
+    }
+    if constexpr (SCORES) {
+      if (cl < n_h) {
+        float* sp = w.scores + ((int64_t)b * a.n_heads + head) * w.n_scores + s * kTile + 8 * g;
+        *(float4v*)sp = (float4v){x[0], x[1], x[2], x[3]};
+        *(float4v*)(sp + 4) = (float4v){x[4], x[5], x[6], x[7]};
+      }
+    }
+    float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+    if (__any(top > m + kRaise)) {
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float nm = fmaxf(m, top);
+      const float f = m == -INFINITY ? 0.0f : exp2f(m - nm);
+      m = nm;
+      lsum *= f;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) o[i] *= f;
+    }
+    const float base = m == -INFINITY ? 0.0f : m;
+    float pr[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      pr[j] = __builtin_amdgcn_exp2f(x[j] - base);
+      lsum += pr[j];
+    }
+    // P in the cache's type for the matrix cores. bf16 keeps 8 bits, fewer than the
+    // output's rounding hides behind, so its remainder goes through a second product
+    // (the matrix cores have the time); fp16 keeps 11.
+    x8 ph, pl;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      ph[j] = (T)pr[j];
+      if constexpr (__is_same(T, bf16_t)) pl[j] = (T)(pr[j] - (float)ph[j]);
+    }
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      uint4v vt;
+#pragma unroll
+      for (int jp = 0; jp < 4; ++jp)
+        vt[jp] = __builtin_amdgcn_perm(r.v[2 * jp + 1][i / 2], r.v[2 * jp][i / 2], (i & 1) ? 0x07060302u : 0x05040100u);
+      const x8 va = __builtin_bit_cast(x8, vt);
+      o[i] = KT::mfma16(va, ph, o[i]);
+      if constexpr (__is_same(T, bf16_t)) o[i] = KT::mfma16(va, pl, o[i]);
+    }
+  };
+
+  Regs ra, rb;
+  int s = split * per + wave;
+  if (s < s_end) {
+    Pages pa = pages(s), pb = pages(s + kWaves);
+    load(s, pa, ra);
+    while (true) {
+      // the next step's rows (the last step loads itself again, unused)
+      const bool more = s + kWaves < s_end;
+      load(more ? s + kWaves : s, more ? pb : pa, rb);
+      Pages pc = pages(s + 2 * kWaves);
+      asm volatile("" ::: "memory");
+      compute(s, pa, ra);
+      if (!more) break;
+      s += kWaves;
+      const bool more2 = s + kWaves < s_end;
+      load(more2 ? s + kWaves : s, more2 ? pc : pb, ra);
+      Pages pd = pages(s + 2 * kWaves);
+      asm volatile("" ::: "memory");
+      compute(s, pb, rb);
+      if (!more2) break;
+      s += kWaves;
+      pa = pc;
+      pb = pd;
+    }
+  }
+
+  // join the waves of the block
+  lsum += __shfl_xor(lsum, 16);
+  lsum += __shfl_xor(lsum, 32);
+  __shared__ float sm[kWaves][16], sl[kWaves][16];
+  __shared__ float so[kWaves][16][16 * VEC + 4];
+  if (g == 0) {
+    sm[wave][cl] = m;
+    sl[wave][cl] = lsum;
+  }
+  if (cl < n_h) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) so[wave][cl][(4 * g + r) * VEC + i] = o[i][r];
+  }
+  __syncthreads();
+  for (int k = threadIdx.x; k < n_h * c.dim; k += 64 * kWaves) {
+    const int hh = k / c.dim, e = k - hh * c.dim;
+    float mm = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < kWaves; ++u) mm = fmaxf(mm, sm[u][hh]);
+    float l = 0.0f, v = 0.0f;
+#pragma unroll
+    for (int u = 0; u < kWaves; ++u) {
+      const float f = sm[u][hh] == -INFINITY ? 0.0f : exp2f(sm[u][hh] - mm);
+      // a wave without a visible slot holds zeros
+      l += f * sl[u][hh];
+      v += f * so[u][hh][e];
+    }
+    const int64_t bh = (int64_t)b * a.n_heads + kvh * group + h0 + hh;
+    if constexpr (SPLIT) {
+      w.o[(bh * w.n_splits + split) * c.dim + e] = v;
+      if (e == 0) {
+        w.ml[(bh * w.n_splits + split) * 2] = mm;
+        w.ml[(bh * w.n_splits + split) * 2 + 1] = l;
+      }
+    } else {
+      ((T*)a.out)[(int64_t)b * a.ldo + (int64_t)(kvh * group + h0 + hh) * c.dim + e] = (T)(l == 0.0f ? 0.0f : v / l);
+    }
+  }
+}
+
+// Joins the splits of one (sequence, key head): block part 0 the outputs of its
+// heads, every part the weights of its steps. Each head's maximum and sum over
+// the splits are found again by every block (a few hundred bytes).
+constexpr int kJoinSteps = 32;  // steps whose weights one block adds
+
+template <typename T>
+__global__ __launch_bounds__(256) void token_join_kernel(KvView c, KvAttnArgs a, TokenWs w, int n_parts) {
+  extern __shared__ float sh[];  // per head of the group: maximum, 1 / sum
+  const int group = a.n_heads / c.n_kv;
+  int id = blockIdx.x;
+  const int part = id % n_parts;
+  id /= n_parts;
+  const int kvh = id % c.n_kv, b = id / c.n_kv;
+  const int64_t bh0 = (int64_t)b * a.n_heads + kvh * group;
+  for (int h = threadIdx.x >> 6; h < group; h += 4) {
+    const float* ml = w.ml + (bh0 + h) * w.n_splits * 2;
+    float mm = -INFINITY, l = 0.0f;
+    for (int s = threadIdx.x & 63; s < w.n_splits; s += 64) mm = fmaxf(mm, ml[2 * s]);
+    for (int o = 32; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor(mm, o));
+    for (int s = threadIdx.x & 63; s < w.n_splits; s += 64)
+      l += ml[2 * s] == -INFINITY ? ml[2 * s + 1] : exp2f(ml[2 * s] - mm) * ml[2 * s + 1];
+    for (int o = 32; o > 0; o >>= 1) l += __shfl_xor(l, o);
+    if ((threadIdx.x & 63) == 0) {
+      sh[2 * h] = mm == -INFINITY ? 0.0f : mm;
+      sh[2 * h + 1] = l == 0.0f ? 0.0f : 1.0f / l;
+    }
+  }
+  __syncthreads();
+  if (part == 0) {
+    for (int k = threadIdx.x; k < group * c.dim; k += 256) {
+      const int h = k / c.dim, e = k - h * c.dim;
+      const float* ml = w.ml + (bh0 + h) * w.n_splits * 2;
+      const float* o = w.o + (bh0 + h) * w.n_splits * c.dim + e;
+      float v = 0.0f;
+      for (int s = 0; s < w.n_splits; ++s)
+        v += ml[2 * s] == -INFINITY ? o[(int64_t)s * c.dim] : exp2f(ml[2 * s] - sh[2 * h]) * o[(int64_t)s * c.dim];
+      ((T*)a.out)[(int64_t)b * a.ldo + (int64_t)(kvh * group + h) * c.dim + e] = (T)(v * sh[2 * h + 1]);
+    }
+  }
+  if (!a.weights) return;
+  const Steps st(c.len(b), a.window, a.sinks);
+  const int s1 = (part + 1) * kJoinSteps < st.total ? (part + 1) * kJoinSteps : st.total;
+  float* wt = a.weights + ((int64_t)b * c.n_kv + kvh) * a.ldw;
+  for (int k = part * kJoinSteps * kTile + threadIdx.x; k < s1 * kTile; k += 256) {
+    const int t = st.slot0(k / kTile) + k % kTile;
+    if (t >= st.n || (t < st.first && t >= a.sinks)) continue;
+    float add = 0.0f;
+    for (int h = 0; h < group; ++h)
+      add += exp2f(w.scores[(bh0 + h) * w.n_scores + k] - sh[2 * h]) * sh[2 * h + 1];
+    wt[t] += add;
+  }
+}
+
+int64_t max_steps(const KvView& c, int64_t window, int64_t sinks) {
+  const int64_t cap = (int64_t)c.max_pages << c.page_shift, all = ceil_div(cap, kTile);
+  if (window <= 0 || window >= cap) return all;
+  const int64_t some = ceil_div(sinks < cap ? sinks : cap, kTile) + window / kTile + 2;
+  return some < all ? some : all;
+}
+
+// Blocks per (sequence, key head, tile of heads).
+int64_t splits_of(const KvView& c, int64_t n_heads, int64_t window, int64_t sinks) {
+  const int64_t base = (int64_t)c.n_seqs * c.n_kv * ceil_div(n_heads / c.n_kv, 16);
+  const int64_t most = ceil_div(max_steps(c, window, sinks), kWaves);
+  int64_t s = ceil_div(1024, base);
+  if (s > most) s = most;
+  if (s > 256) s = 256;
+  return s < 1 ? 1 : s;
+}
+
+TokenWs layout(const KvView& c, int64_t n_heads, int64_t window, int64_t sinks, bool weights, void* ws, size_t* bytes) {
+  TokenWs w{};
+  w.n_splits = (int)splits_of(c, n_heads, window, sinks);
+  w.n_scores = (int)(max_steps(c, window, sinks) * kTile);
+  const int64_t rows = (int64_t)c.n_seqs * n_heads;
+  float* p = (float*)ws;
+  size_t n = 0;
+  if (w.n_splits > 1 || weights) {
+    w.scores = p + n;  // first: 16-byte aligned
+    if (weights) n += (size_t)rows * w.n_scores;
+    w.o = p + n;
+    n += (size_t)rows * w.n_splits * c.dim;
+    w.ml = p + n;
+    n += (size_t)rows * w.n_splits * 2;
+  }
+  if (bytes) *bytes = n * sizeof(float);
+  return w;
+}
+
+template <typename T, int KS, int VEC>
+gptq_status_t launch(const KvView& c, const KvAttnArgs& a, const TokenWs& w, hipStream_t st) {
+  const int64_t blocks = (int64_t)c.n_seqs * c.n_kv * ceil_div(a.n_heads / c.n_kv, 16) * w.n_splits;
+  if (blocks * 64 * kWaves >= (int64_t)1 << 32) return GPTQ_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)blocks), blk(64 * kWaves);
+  if (a.weights)
+    hipLaunchKernelGGL((token_kernel<T, KS, VEC, true, true>), grid, blk, 0, st, c, a, w);
+  else if (w.n_splits > 1)
+    hipLaunchKernelGGL((token_kernel<T, KS, VEC, true, false>), grid, blk, 0, st, c, a, w);
+  else
+    hipLaunchKernelGGL((token_kernel<T, KS, VEC, false, false>), grid, blk, 0, st, c, a, w);
+  GPTQ_CHECK_LAUNCH();
+  return GPTQ_OK;
+}
+
+template <typename T>
+gptq_status_t token_enqueue(const KvView& c, const KvAttnArgs& a, void* ws, hipStream_t st) {
+  const TokenWs w = layout(c, a.n_heads, a.window, a.sinks, a.weights != nullptr, ws, nullptr);
+  const int64_t parts = a.weights ? ceil_div(w.n_scores / kTile, kJoinSteps) : 1;
+  const int64_t jblocks = (int64_t)c.n_seqs * c.n_kv * parts;
+  if (jblocks * 256 >= (int64_t)1 << 32) return GPTQ_ERR_UNSUPPORTED;
+  gptq_status_t rc;
+  if (c.dim <= 64)
+    rc = launch<T, 2, 4>(c, a, w, st);
+  else if (c.dim <= 96)
+    rc = launch<T, 3, 8>(c, a, w, st);
+  else
+    rc = launch<T, 4, 8>(c, a, w, st);
+  if (rc != GPTQ_OK || (w.n_splits == 1 && !a.weights)) return rc;
+  hipLaunchKernelGGL(token_join_kernel<T>, dim3((unsigned)jblocks), dim3(256),
+                     2 * sizeof(float) * (a.n_heads / c.n_kv), st, c, a, w, (int)parts);
+  GPTQ_CHECK_LAUNCH();
+  return GPTQ_OK;
+}
+
+}  // namespace
+
+size_t kv_token_workspace_bytes(const KvView& c, int64_t n_heads, int64_t window, int64_t sinks, bool weights) {
+  size_t bytes = 0;
+  layout(c, n_heads, window, sinks, weights, nullptr, &bytes);
+  return bytes;
+}
+
+gptq_status_t kv_token_enqueue(const KvView& c, const KvAttnArgs& a, void* ws, hipStream_t st) {
+  TraceScope tr(st, GPTQ_TRACE_KV_ATTENTION);
+  return c.bf16 ? token_enqueue<bf16_t>(c, a, ws, st) : token_enqueue<half_t>(c, a, ws, st);
+}
+
+}  // namespace gptq

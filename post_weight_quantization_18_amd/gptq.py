@@ -13,6 +13,10 @@ Entry points (same names as include/gptq.h):
     quantize_layer_ordered(W, U, perm, bits, group_size, grid, static_groups)
     dequant_gemv(qcodes, scales, zeros, bits, group_size, x)   y = W_hat x, one token
     pack_codes(codes, bits)
+    kv_append(k, v, page_table, lens, k_new, v_new, cu_seqlens)   new rows into a paged key-value cache
+    paged_attention(q, k, v, page_table, lens, ...)   one new token per sequence over its pages
+    paged_prefill(q, k, v, page_table, lens, cu_seqlens, ...)   prompts, or the next chunks of them
+    kv_evict(k, v, page_table, lens, weights, budget, new_pages, ...)   the least attended slots leave
     trace_start(), trace_stop()                device time per kernel family (instrumentation)
 and quantize(W, x_chunks, ...) which runs the stages of one layer (natural
 order, or act-order with act_order=True).
@@ -31,7 +35,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("GPTQ_MI355X_LIB") or os.path.join(_HERE, "libgptq_mi355x.so")
 
 GPTQ_OK, GPTQ_ERR_INVALID_ARG, GPTQ_ERR_WORKSPACE, GPTQ_ERR_HIP, GPTQ_ERR_UNSUPPORTED = range(5)
-GPTQ_F16, GPTQ_F32, GPTQ_F64 = 0, 1, 2
+GPTQ_F16, GPTQ_F32, GPTQ_F64, GPTQ_BF16 = 0, 1, 2, 3
 GPTQ_GRID_ASYM_MINMAX, GPTQ_GRID_TERNARY, GPTQ_GRID_SYM_MINMAX = 0, 1, 2
 WS_ACCUMULATE_HESSIAN, WS_PREPARE_HINV, WS_QUANTIZE_LAYER = 0, 1, 2
 
@@ -39,8 +43,9 @@ EXPORTED = ["gptq_abi_version", "gptq_status_string", "gptq_workspace_bytes", "g
             "gptq_prepare_hinv", "gptq_quantize_layer", "gptq_act_order", "gptq_permute_hessian",
             "gptq_quantize_layer_ordered", "gptq_dequant_gemv", "gptq_pack_codes", "gptq_trace_start",
             "gptq_trace_stop", "gptq_trace_family", "gptq_accumulate_hessian_noalloc", "gptq_prepare_hchol",
-            "gptq_gemv_prepare_act_order", "gptq_dequant_gemv_perm"]
-TRACE_FAMILIES = 15
+            "gptq_gemv_prepare_act_order", "gptq_dequant_gemv_perm", "gptq_kv_append", "gptq_kv_workspace_bytes",
+            "gptq_paged_attention", "gptq_paged_prefill", "gptq_kv_evict"]
+TRACE_FAMILIES = 18
 
 
 GPTQ_FACTOR_HINV_CHOL, GPTQ_FACTOR_H_CHOL = 0, 1
@@ -50,6 +55,17 @@ _FACTOR = {"U": GPTQ_FACTOR_HINV_CHOL, "R": GPTQ_FACTOR_H_CHOL}
 class QCfg(ctypes.Structure):
     _fields_ = [("bits", ctypes.c_int32), ("grid", ctypes.c_int32), ("group_size", ctypes.c_int32),
                 ("block_size", ctypes.c_int32), ("factor", ctypes.c_int32)]
+
+
+class KvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("n_pages", ctypes.c_int64), ("page_stride", ctypes.c_int64)]
+
+
+class KvSeqs(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("ld_table", ctypes.c_int64), ("max_pages", ctypes.c_int64),
+                ("lens", ctypes.c_void_p), ("n_seqs", ctypes.c_int64)]
 
 
 _lib = None
@@ -96,6 +112,17 @@ def load_library(path: str = LIB_PATH):
     lib.gptq_pack_codes.argtypes = [vp, i64, i64, i32, vp, vp]
     lib.gptq_accumulate_hessian_noalloc.restype = i32
     lib.gptq_accumulate_hessian_noalloc.argtypes = [vp, i32, i64, i64, vp, i64, i64, i32, vp]
+    f32, pc, ps = ctypes.c_float, ctypes.POINTER(KvCache), ctypes.POINTER(KvSeqs)
+    lib.gptq_kv_append.restype = i32
+    lib.gptq_kv_append.argtypes = [pc, ps, vp, i64, vp, i64, vp, i64, vp]
+    lib.gptq_kv_workspace_bytes.restype = sz
+    lib.gptq_kv_workspace_bytes.argtypes = [pc, ps, i64, i64, i64, i64, i32]
+    lib.gptq_paged_attention.restype = i32
+    lib.gptq_paged_attention.argtypes = [pc, ps, vp, i64, i64, f32, i64, i64, vp, i64, vp, i64, vp, sz, vp]
+    lib.gptq_paged_prefill.restype = i32
+    lib.gptq_paged_prefill.argtypes = [pc, ps, vp, i64, vp, i64, i64, f32, i64, i64, vp, i64, vp, i64, vp, sz, vp]
+    lib.gptq_kv_evict.restype = i32
+    lib.gptq_kv_evict.argtypes = [pc, ps, vp, i64, i64, i64, i64, vp, i64, vp, i64, vp, vp, i64, vp, vp]
     lib.gptq_trace_start.restype = i32
     lib.gptq_trace_start.argtypes = []
     lib.gptq_trace_stop.restype = i32
@@ -385,6 +412,193 @@ def pack_codes(codes: torch.Tensor, bits: int) -> torch.Tensor:
     out = torch.empty(m, d * bits // 32, dtype=torch.int32, device=codes.device)
     _check(lib.gptq_pack_codes(_ptr(codes), m, d, bits, _ptr(out), _stream(codes.device)), "gptq_pack_codes")
     return out
+
+
+_KV_DT = {torch.float16: GPTQ_F16, torch.bfloat16: GPTQ_BF16}
+
+
+def _kv(k, v, page_table, lens, *others):
+    """The cache and its sequences as the library takes them, checked: dtypes,
+    shapes and one device for these and every tensor of `others` (or None)."""
+    _need_cuda(k, "k")
+    dev = k.device
+    for t in (v, page_table, lens, *others):
+        if t is not None and t.device != dev:
+            raise ValueError("every tensor must be on the cache's device")
+    if k.dtype not in _KV_DT or v.dtype != k.dtype:
+        raise ValueError("k and v must be fp16 or bf16, both the same")
+    if k.dim() != 4 or v.shape != k.shape:
+        raise ValueError("k and v must be [n_pages, n_kv_heads, page_size, head_dim]")
+    n_pages, n_kv, ps, dim = k.shape
+    if k.stride() != v.stride() or k.stride()[1:] != (ps * dim, dim, 1):
+        raise ValueError("k and v: equal strides, contiguous within a page")
+    if page_table.dtype != torch.int32 or lens.dtype != torch.int32:
+        raise ValueError("page_table and lens must be int32")
+    if page_table.dim() != 2 or lens.dim() != 1 or page_table.shape[0] != lens.shape[0]:
+        raise ValueError("page_table [n_seqs, max_pages], lens [n_seqs]")
+    if page_table.stride(1) != 1 or (lens.stride(0) != 1 and lens.shape[0] > 1):
+        raise ValueError("page_table rows and lens must be contiguous")
+    n_seqs, max_pages = page_table.shape
+    cache = KvCache(k.data_ptr(), v.data_ptr(), _KV_DT[k.dtype], ps, n_kv, dim, n_pages,
+                    k.stride(0) if n_pages > 1 else n_kv * ps * dim)
+    # one row: its stride says nothing
+    seqs = KvSeqs(page_table.data_ptr(), page_table.stride(0) if n_seqs > 1 else max_pages, max_pages,
+                  lens.data_ptr(), n_seqs)
+    return cache, seqs
+
+
+def _rows(t, name, dtype, heads, dim):
+    """Row stride of new tokens' rows [n, heads, dim], contiguous within a row."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must have the cache's dtype")
+    if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [n, heads, head_dim] of the cache's head_dim")
+    if t.stride(2) != 1 or (t.stride(1) != dim and t.shape[1] > 1):
+        raise ValueError(f"{name} rows must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * dim
+
+
+def _cu(cu, n_seqs):
+    if cu.dtype != torch.int32 or cu.dim() != 1 or cu.shape[0] != n_seqs + 1 or not cu.is_contiguous():
+        raise ValueError("cu_seqlens must be contiguous int32 [n_seqs + 1]")
+    return cu.data_ptr()
+
+
+def _weights(w, name, n_seqs, n_kv, slots):
+    """Row stride of accumulated weights [n_seqs, n_kv, >= slots]."""
+    if w.dtype != torch.float32 or w.dim() != 3 or w.shape[0] != n_seqs or w.shape[1] != n_kv or w.shape[2] < slots:
+        raise ValueError(f"{name} must be fp32 [n_seqs, n_kv_heads, >= max_pages * page_size]")
+    if not w.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return w.shape[2]
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor, k_new: torch.Tensor,
+              v_new: torch.Tensor, cu_seqlens: torch.Tensor | None = None):
+    """New tokens' keys and values into the pages of their sequences. k, v [n_pages,
+    n_kv_heads, page_size, head_dim] fp16 or bf16; page_table int32 [n_seqs,
+    max_pages]; lens int32 [n_seqs], the new tokens counted; k_new, v_new [n,
+    n_kv_heads, head_dim], sequence b's rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1
+    (int32 [n_seqs + 1]; None: one row per sequence)."""
+    lib = load_library()
+    cache, seqs = _kv(k, v, page_table, lens, k_new, v_new, cu_seqlens)
+    ldk = _rows(k_new, "k_new", k.dtype, k.shape[1], k.shape[3])
+    ldv = _rows(v_new, "v_new", k.dtype, k.shape[1], k.shape[3])
+    if k_new.shape[0] != v_new.shape[0]:
+        raise ValueError("k_new and v_new must have the same tokens")
+    cu = _cu(cu_seqlens, seqs.n_seqs) if cu_seqlens is not None else None
+    with _on(k.device):
+        _check(lib.gptq_kv_append(cache, seqs, k_new.data_ptr(), ldk, v_new.data_ptr(), ldv, cu, k_new.shape[0],
+                                  torch.cuda.current_stream(k.device).cuda_stream), "gptq_kv_append")
+
+
+class _Here:
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        pass
+
+
+_HERE_GUARD = _Here()
+
+
+def _on(device):
+    """The device of the call's tensors made current (it usually is already)."""
+    return _HERE_GUARD if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def kv_workspace_bytes(k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor, n_heads: int,
+                       window: int = 0, sinks: int = 0, n_tokens: int = 0, weights: bool = False) -> int:
+    """Workspace of paged_attention (n_tokens = 0) or of paged_prefill with n_tokens rows."""
+    cache, seqs = _kv(k, v, page_table, lens)
+    return int(load_library().gptq_kv_workspace_bytes(cache, seqs, n_heads, window, sinks, n_tokens, int(weights)))
+
+
+def _attend(fn, name, q, k, v, page_table, lens, cu_seqlens, scale, window, sinks, weights, out, workspace):
+    lib = load_library()
+    cache, seqs = _kv(k, v, page_table, lens, q, cu_seqlens, weights, out, workspace)
+    dim = k.shape[3]
+    ldq = _rows(q, "q", k.dtype, None, dim)
+    n, heads = q.shape[0], q.shape[1]
+    if out is None:
+        out = torch.empty(n, heads, dim, dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    ldo = _rows(out, "out", k.dtype, heads, dim)
+    wp, ldw = None, 0
+    if weights is not None:
+        ldw = _weights(weights, "weights", seqs.n_seqs, k.shape[1], seqs.max_pages * k.shape[2])
+        wp = weights.data_ptr()
+    if scale is None:
+        scale = dim ** -0.5
+    rows = () if cu_seqlens is None else (_cu(cu_seqlens, seqs.n_seqs), n)
+    nbytes = lib.gptq_kv_workspace_bytes(cache, seqs, heads, window, sinks, n if rows else 0, int(weights is not None))
+    with _on(k.device):
+        ws = _workspace(nbytes, k.device, workspace)
+        _check(fn(lib)(cache, seqs, q.data_ptr(), ldq, *rows, heads, scale, window, sinks, wp, ldw, out.data_ptr(), ldo,
+                       ws.data_ptr() if ws is not None else None, nbytes,
+                       torch.cuda.current_stream(k.device).cuda_stream), name)
+    return out
+
+
+def paged_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,
+                    scale: float | None = None, window: int = 0, sinks: int = 0, weights: torch.Tensor | None = None,
+                    out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of one new token per sequence (its key and value already appended):
+    out [n_seqs, n_heads, head_dim] in q's dtype. The token sees its whole sequence,
+    or with a window the last `window` slots and the first `sinks`. scale defaults
+    to head_dim^-0.5. weights fp32 [n_seqs, n_kv_heads, slots] (slots >= max_pages *
+    page_size): every visible slot's attention weight is added, summed over the heads
+    that share its key."""
+    if q.dim() == 3 and q.shape[0] != page_table.shape[0]:
+        raise ValueError("q must have one row per sequence")
+    return _attend(lambda lib: lib.gptq_paged_attention, "gptq_paged_attention", q, k, v, page_table, lens, None, scale,
+                   window, sinks, weights, out, workspace)
+
+
+def paged_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,
+                  cu_seqlens: torch.Tensor, scale: float | None = None, window: int = 0, sinks: int = 0,
+                  weights: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Causal attention of prompts, or of the next chunks of longer ones, over the
+    pages: rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of q [n, n_heads, head_dim] are
+    the last tokens of sequence b. Rows behind the last sequence stay as `out` held
+    them. Other arguments as paged_attention."""
+    return _attend(lambda lib: lib.gptq_paged_prefill, "gptq_paged_prefill", q, k, v, page_table, lens, cu_seqlens,
+                   scale, window, sinks, weights, out, workspace)
+
+
+def kv_evict(k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor, weights: torch.Tensor,
+             budget: int, new_pages: torch.Tensor, sinks: int = 0, recent: int = 0):
+    """Sequences longer than budget keep, per kv head, the first `sinks`, the last
+    `recent` and the most attended other slots (weights, as the attention calls add
+    them), in order, moved to new_pages int32 [n_seqs, >= ceil(budget / page_size)]
+    (free pages). Returns (page_table, lens, weights, kept): the table and lengths
+    to go on with, the weights in the new order (0 behind the last slot), and
+    int32 [n_seqs, n_kv_heads, budget] the old slot of every new one (-1 behind the
+    last)."""
+    lib = load_library()
+    cache, seqs = _kv(k, v, page_table, lens, weights, new_pages)
+    n_seqs, max_pages = page_table.shape
+    n_kv, ps = k.shape[1], k.shape[2]
+    ldw = _weights(weights, "weights", n_seqs, n_kv, max_pages * ps)
+    if new_pages.dtype != torch.int32 or new_pages.dim() != 2 or new_pages.shape[0] != n_seqs or \
+            (new_pages.stride(1) != 1 and new_pages.shape[1] > 1):
+        raise ValueError("new_pages must be int32 [n_seqs, pages], rows contiguous")
+    if budget < 1:
+        raise ValueError("budget must be positive")
+    dev = k.device
+    table_out = torch.empty(n_seqs, max_pages, dtype=torch.int32, device=dev)
+    lens_out = torch.empty(n_seqs, dtype=torch.int32, device=dev)
+    weights_out = torch.empty(n_seqs, n_kv, max_pages * ps, dtype=torch.float32, device=dev)
+    kept = torch.empty(n_seqs, n_kv, budget, dtype=torch.int32, device=dev)
+    with _on(dev):
+        _check(lib.gptq_kv_evict(cache, seqs, weights.data_ptr(), ldw, budget, sinks, recent, new_pages.data_ptr(),
+                                 new_pages.stride(0) if n_seqs > 1 else new_pages.shape[1], table_out.data_ptr(),
+                                 max_pages, lens_out.data_ptr(), weights_out.data_ptr(), max_pages * ps,
+                                 kept.data_ptr(), torch.cuda.current_stream(dev).cuda_stream), "gptq_kv_evict")
+    return table_out, lens_out, weights_out, kept
 
 
 def trace_start():

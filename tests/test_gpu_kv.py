@@ -1,0 +1,396 @@
+"""The paged key-value cache on the GPU: append, attention of one token and of
+prompts (windows, sinks, shared heads, accumulated weights), eviction, and a run of
+them together, against plain 64-bit arithmetic."""
+
+import numpy as np
+import pytest
+import torch
+
+import kv_reference as R
+from post_weight_quantization_18_amd import gptq as G
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+DT = {"fp16": torch.float16, "bf16": torch.bfloat16}
+HALF_STEP = {"fp16": 2.0 ** -11, "bf16": 2.0 ** -8}
+
+
+def _randn(gen, *shape):
+    return torch.randn(*shape, generator=gen, dtype=torch.float32)
+
+
+class Case:
+    """Sequences of given lengths in a cache whose unused rows hold NaN and infinities."""
+
+    def __init__(self, dtype, lens, heads, kv, dim, ps, seed=0, spare=2, max_pages=None):
+        self.dtype, self.lens, self.heads, self.kv, self.dim, self.ps = dtype, list(lens), heads, kv, dim, ps
+        g = torch.Generator().manual_seed(seed)
+        n = len(lens)
+        self.max_pages = max_pages or max(1, -(-max(list(lens) + [1]) // ps))
+        used = [-(-x // ps) for x in lens]
+        self.n_pages = sum(used) + spare
+        order = torch.randperm(self.n_pages, generator=g)
+        self.free = order[sum(used):].tolist()
+        table = torch.full((n, self.max_pages), 1 << 30, dtype=torch.int32)  # entries behind a length are not read
+        self.k = torch.full((self.n_pages, kv, ps, dim), float("nan"), dtype=DT[dtype])
+        self.v = torch.full((self.n_pages, kv, ps, dim), float("inf"), dtype=DT[dtype])
+        at = 0
+        for b, x in enumerate(lens):
+            table[b, :used[b]] = order[at:at + used[b]].to(torch.int32)
+            at += used[b]
+            for t in range(x):
+                self.k[table[b, t // ps], :, t % ps] = _randn(g, kv, dim).to(DT[dtype])
+                self.v[table[b, t // ps], :, t % ps] = _randn(g, kv, dim).to(DT[dtype])
+        self.table = table
+        self.gen = g
+
+    def gpu(self):
+        return (self.k.to(DEV), self.v.to(DEV), self.table.to(DEV),
+                torch.tensor(self.lens, dtype=torch.int32, device=DEV))
+
+    def queries(self, n):
+        return (1.5 * _randn(self.gen, n, self.heads, self.dim)).to(DT[self.dtype])
+
+    def weights(self):
+        return torch.rand(len(self.lens), self.kv, self.max_pages * self.ps, generator=self.gen)
+
+    def expect(self, q, cu, window, sinks, u_p, scale=None):
+        """out, its tolerance, added weights, their tolerance for q's rows cu."""
+        scale = self.dim ** -0.5 if scale is None else scale
+        qn = q.double().numpy()
+        kn, vn = self.k.double().numpy(), self.v.double().numpy()
+        out, tol = np.zeros(qn.shape), np.zeros(qn.shape)
+        w = np.zeros((len(self.lens), self.kv, self.max_pages * self.ps))
+        wt = np.zeros_like(w)
+        for b, n in enumerate(self.lens):
+            kk, there = R.gather(kn, self.table[b].numpy(), n)
+            vv, _ = R.gather(vn, self.table[b].numpy(), n)
+            m = cu[b + 1] - cu[b]
+            for j in range(m):
+                o, a, t, at = R.attend(qn[cu[b] + j], kk, vv, there, n - m + j, scale, window, sinks, u_p,
+                                       HALF_STEP[self.dtype])
+                out[cu[b] + j], tol[cu[b] + j] = o, t
+                w[b, :, :n] += a
+                wt[b, :, :n] += at + m * R.U * a
+        return out, tol, w, wt
+
+
+def _near(got, want, tol, what):
+    got = got.double().cpu().numpy()
+    assert np.isfinite(got).all(), what
+    off = np.abs(got - want) / np.maximum(tol, 1e-300)
+    off[(got == want)] = 0.0
+    assert off.max() <= 1.0, f"{what}: {off.max():.3g} times the tolerance at {np.unravel_index(off.argmax(), off.shape)}"
+
+
+TOKEN = [
+    # dtype, lens, heads, kv heads, dim, page size, window, sinks
+    ("fp16", [0, 1, 7, 8, 9, 31, 32, 33], 2, 2, 64, 8, 0, 0),
+    ("bf16", [5, 0, 130, 64], 4, 2, 128, 16, 0, 0),
+    ("fp16", [300, 129, 1], 3, 1, 80, 16, 0, 0),
+    ("fp16", [257, 40], 40, 2, 96, 32, 0, 0),          # 20 heads a key: two tiles of heads
+    ("bf16", [513], 7, 1, 72, 64, 0, 0),
+    ("fp16", [200, 33, 17, 3], 2, 2, 24, 8, 0, 0),
+    ("fp16", [300, 31, 64, 5], 2, 1, 128, 16, 33, 4),
+    ("bf16", [300, 200, 90], 4, 4, 64, 32, 1, 0),
+    ("fp16", [400, 100, 66], 2, 2, 128, 128, 64, 65),
+    ("fp16", [90, 200], 2, 2, 8, 16, 17, 500),
+    ("bf16", [1025], 2, 2, 128, 256, 7, 1),
+    ("fp16", [2300, 700], 1, 1, 128, 64, 0, 0),        # many splits
+]
+
+
+@pytest.mark.parametrize("weights", [False, True])
+@pytest.mark.parametrize("case", TOKEN, ids=lambda c: "-".join(map(str, c)).replace(" ", ""))
+def test_one_token(case, weights):
+    dtype, lens, heads, kv, dim, ps, window, sinks = case
+    print(f"[case] token {case} weights={weights}", flush=True)
+    c = Case(dtype, lens, heads, kv, dim, ps)
+    if window:  # slots that nothing sees may hold anything
+        for b, n in enumerate(lens):
+            for t in np.nonzero(~R.visible(n - 1, n, window, sinks))[0]:
+                c.v[c.table[b, t // ps], :, t % ps] = float("nan")
+                c.k[c.table[b, t // ps], :, t % ps] = float("inf")
+    q = c.queries(len(lens))
+    k, v, table, ln = c.gpu()
+    w = c.weights() if weights else None
+    wd = w.to(DEV) if weights else None
+    out = G.paged_attention(q.to(DEV), k, v, table, ln, window=window, sinks=sinks, weights=wd)
+    u_p = 2.0 ** -11 if dtype == "fp16" else 2.0 ** -16
+    for b, n in enumerate(lens):  # the expectation's products: 0 x NaN of hidden slots left out
+        for t in np.nonzero(~R.visible(n - 1, n, window, sinks))[0]:
+            c.v[c.table[b, t // ps], :, t % ps] = 0.0
+            c.k[c.table[b, t // ps], :, t % ps] = 0.0
+    want, tol, added, wtol = c.expect(q, range(len(lens) + 1), window, sinks, u_p)
+    _near(out, want, tol, "out")
+    if weights:
+        total = w.double().numpy() + added
+        _near(wd, total, wtol + R.U * np.abs(total) * (added > 0), "weights")
+
+
+PROMPT = [
+    # dtype, lens, new tokens, heads, kv heads, dim, page size, window, sinks
+    ("fp16", [1, 2, 0, 65, 130], [1, 2, 0, 65, 130], 2, 2, 64, 8, 0, 0),
+    ("bf16", [70, 200], [70, 129], 4, 2, 128, 16, 0, 0),
+    ("fp16", [300, 33], [40, 33], 3, 1, 80, 32, 0, 0),
+    ("fp16", [260], [260], 2, 1, 96, 64, 50, 3),
+    ("bf16", [300, 257], [300, 20], 2, 2, 64, 16, 1, 0),
+    ("fp16", [400], [200], 1, 1, 128, 128, 100, 130),
+    ("fp16", [150, 90], [150, 90], 2, 2, 24, 8, 17, 70),
+    ("bf16", [129, 5], [129, 5], 7, 1, 40, 16, 0, 0),
+    ("fp16", [3, 20], [10, 25], 2, 2, 64, 8, 0, 0),     # more new tokens than slots: rows that see nothing
+]
+
+
+@pytest.mark.parametrize("weights", [False, True])
+@pytest.mark.parametrize("case", PROMPT, ids=lambda c: "-".join(map(str, c)).replace(" ", ""))
+def test_prompts(case, weights):
+    dtype, lens, new, heads, kv, dim, ps, window, sinks = case
+    print(f"[case] prompt {case} weights={weights}", flush=True)
+    c = Case(dtype, lens, heads, kv, dim, ps)
+    cu = [0]
+    for x in new:
+        cu.append(cu[-1] + x)
+    q = c.queries(cu[-1] + 3)  # three rows behind the last sequence
+    k, v, table, ln = c.gpu()
+    w = c.weights() if weights else None
+    wd = w.to(DEV) if weights else None
+    out = torch.full_like(q, 7.0).to(DEV)
+    G.paged_prefill(q.to(DEV), k, v, table, ln, torch.tensor(cu, dtype=torch.int32, device=DEV), window=window,
+                    sinks=sinks, weights=wd, out=out)
+    assert (out[cu[-1]:] == 7.0).all()
+    want, tol, added, wtol = c.expect(q[:cu[-1]], cu, window, sinks, HALF_STEP[dtype])
+    _near(out[:cu[-1]], want, tol, "out")
+    if weights:
+        total = w.double().numpy() + added
+        _near(wd, total, wtol + R.U * np.abs(total) * (added > 0), "weights")
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_prompt_rows_do_not_see_values_that_are_not_finite_behind_their_mask(dtype):
+    """A NaN or infinite value reaches the rows that see its slot and no other."""
+    print(f"[case] prompt with non-finite values {dtype}", flush=True)
+    c = Case(dtype, [150], 2, 1, 64, 16)
+    q = c.queries(150)
+    window, sinks = 40, 2
+    bad = {30: float("nan"), 31: float("inf"), 100: float("-inf"), 149: float("nan")}
+    for t, x in bad.items():
+        c.v[c.table[0, t // 16], 0, t % 16, 5] = x
+        c.k[c.table[0, t // 16], 0, t % 16] *= 0.1
+    k, v, table, ln = c.gpu()
+    out = G.paged_prefill(q.to(DEV), k, v, table, ln, torch.tensor([0, 150], dtype=torch.int32, device=DEV),
+                          window=window, sinks=sinks).double().cpu().numpy()
+    for t in bad:
+        c.v[c.table[0, t // 16], 0, t % 16, 5] = 0.0
+    want, tol, _, _ = c.expect(q, [0, 150], window, sinks, HALF_STEP[dtype])
+    for p in range(150):
+        sees = [x for t, x in bad.items() if R.visible(p, 150, window, sinks)[t]]
+        for h in range(2):
+            others = np.arange(64) != 5
+            assert (np.abs(out[p, h] - want[p, h]) <= tol[p, h])[others].all(), p
+            got = out[p, h, 5]
+            if not sees:
+                assert abs(got - want[p, h, 5]) <= tol[p, h, 5], p
+            elif any(np.isnan(x) for x in sees) or len(set(sees)) > 1:
+                assert np.isnan(got), p
+            else:
+                assert got == sees[0], p
+
+
+def test_entries_outside_the_cache_hold_no_slots():
+    print("[case] bad page entries", flush=True)
+    c = Case("fp16", [100, 70], 4, 2, 64, 8)
+    for b, i, x in ((0, 3, -1), (0, 12, c.n_pages), (1, 0, 2 ** 31 - 1), (1, 8, -2 ** 31)):
+        c.table[b, i] = x
+    k, v, table, ln = c.gpu()
+    q = c.queries(2)
+    w = c.weights()
+    wd = w.to(DEV)
+    out = G.paged_attention(q.to(DEV), k, v, table, ln, weights=wd)
+    want, tol, added, wtol = c.expect(q, [0, 1, 2], 0, 0, 2.0 ** -11)
+    _near(out, want, tol, "token")
+    _near(wd, w.double().numpy() + added, wtol + 4 * R.U, "token weights")
+    q = c.queries(80)
+    wd = w.to(DEV)
+    out = G.paged_prefill(q.to(DEV), k, v, table, ln, torch.tensor([0, 60, 80], dtype=torch.int32, device=DEV),
+                          weights=wd)
+    want, tol, added, wtol = c.expect(q, [0, 60, 80], 0, 0, 2.0 ** -11)
+    _near(out, want, tol, "prompt")
+    _near(wd, w.double().numpy() + added, wtol + 4 * R.U * (1 + added), "prompt weights")
+    # a table of nothing but bad entries: nothing is seen, nothing is written
+    none = torch.full_like(table, -1)
+    assert (G.paged_attention(q[:2].to(DEV), k, v, none, ln) == 0).all()
+    k0, v0 = k.clone(), v.clone()
+    G.kv_append(k, v, none, ln, torch.zeros(2, 2, 64, dtype=torch.float16, device=DEV),
+                torch.zeros(2, 2, 64, dtype=torch.float16, device=DEV))
+    assert torch.equal(k.view(torch.int16), k0.view(torch.int16)) and torch.equal(v.view(torch.int16), v0.view(torch.int16))
+
+
+def test_lengths_outside_the_table_are_cut():
+    print("[case] lengths out of range", flush=True)
+    c = Case("fp16", [32, 32], 2, 2, 64, 8)
+    k, v, table, ln = c.gpu()
+    q = c.queries(2)
+    far = torch.tensor([-5, 10 ** 9], dtype=torch.int32, device=DEV)
+    out = G.paged_attention(q.to(DEV), k, v, table, far)
+    assert (out[0] == 0).all()
+    assert torch.equal(out[1], G.paged_attention(q.to(DEV), k, v, table, ln)[1])
+    k0 = k.clone()
+    new = torch.ones(2, 2, 64, dtype=torch.float16, device=DEV)
+    G.kv_append(k, v, table, far, new, new)
+    assert torch.equal(k.view(torch.int16), k0.view(torch.int16))
+
+
+def test_strided_rows_interleaved_pages_and_a_part_of_a_table():
+    """q, k_new and v_new as slices of one fused projection, the output as a slice, k
+    and v interleaved in one allocation, the table a part of a wider one."""
+    print("[case] strides", flush=True)
+    c = Case("fp16", [50, 33, 17], 4, 2, 64, 16)
+    n_pages = c.n_pages
+    both = torch.full((n_pages, 2, 2, 16, 64), float("nan"), dtype=torch.float16, device=DEV)
+    k, v = both[:, 0], both[:, 1]
+    k.copy_(c.k)
+    v.copy_(c.v)
+    wide = torch.full((3, c.max_pages + 5), 1 << 30, dtype=torch.int32, device=DEV)
+    table = wide[:, 2:2 + c.max_pages]
+    table.copy_(c.table)
+    ln = torch.tensor(c.lens, dtype=torch.int32, device=DEV)
+    fused = (1.5 * _randn(c.gen, 3, (4 + 2 + 2) * 64)).half().to(DEV)
+    q = fused[:, :256].view(3, 4, 64)
+    kn, vn = fused[:, 256:384].view(3, 2, 64), fused[:, 384:].view(3, 2, 64)
+    G.kv_append(k, v, table, ln, kn, vn)
+    for b, n in enumerate(c.lens):
+        c.k[c.table[b, (n - 1) // 16], :, (n - 1) % 16] = kn[b].cpu()
+        c.v[c.table[b, (n - 1) // 16], :, (n - 1) % 16] = vn[b].cpu()
+    assert torch.equal(k.cpu().view(torch.int16), c.k.view(torch.int16))
+    assert torch.equal(v.cpu().view(torch.int16), c.v.view(torch.int16))
+    big = torch.full((3, 320), 9.0, dtype=torch.float16, device=DEV)
+    out = big[:, 32:288].view(3, 4, 64)
+    G.paged_attention(q, k, v, table, ln, out=out)
+    want, tol, _, _ = c.expect(q.cpu(), [0, 1, 2, 3], 0, 0, 2.0 ** -11)
+    _near(out, want, tol, "out")
+    assert (big[:, :32] == 9).all() and (big[:, 288:] == 9).all()
+    out2 = G.paged_prefill(q, k, v, table, ln, torch.tensor([0, 1, 2, 3], dtype=torch.int32, device=DEV), out=out)
+    _near(out2, want, tol, "prefill of one row each")
+
+
+def test_offsets_past_32_bits():
+    """Pages whose elements lie more than 2^32 from the cache's start."""
+    print("[case] far pages", flush=True)
+    n_pages, kv, ps, dim = 140000, 2, 128, 128
+    k = torch.empty(n_pages, kv, ps, dim, dtype=torch.float16, device=DEV)   # 9 GB
+    v = torch.empty_like(k)
+    g = torch.Generator().manual_seed(1)
+    pages = torch.tensor([[139999, 131100, 0, 139998]], dtype=torch.int32)
+    new = _randn(g, 400, kv, dim).half(), _randn(g, 400, kv, dim).half()
+    ln = torch.tensor([400], dtype=torch.int32, device=DEV)
+    cu = torch.tensor([0, 400], dtype=torch.int32, device=DEV)
+    t = pages.to(DEV)
+    G.kv_append(k, v, t, ln, new[0].to(DEV), new[1].to(DEV), cu)
+    c = Case("fp16", [400], 2, 2, 128, 128)
+    for i in range(400):
+        c.k[c.table[0, i // 128], :, i % 128] = new[0][i]
+        c.v[c.table[0, i // 128], :, i % 128] = new[1][i]
+    assert torch.equal(k[139999].cpu(), c.k[c.table[0, 0]])
+    q = c.queries(1)
+    want, tol, _, _ = c.expect(q, [0, 1], 0, 0, 2.0 ** -11)
+    _near(G.paged_attention(q.to(DEV), k, v, t, ln), want, tol, "token")
+    _near(G.paged_prefill(q.to(DEV), k, v, t, ln, torch.tensor([0, 1], dtype=torch.int32, device=DEV)), want, tol,
+          "prompt")
+    w = torch.rand(1, 2, 512, generator=g).to(DEV)
+    into = torch.tensor([[139000, 5]], dtype=torch.int32, device=DEV)
+    table, lens, _, kept = G.kv_evict(k, v, t, ln, w, 200, into, sinks=1, recent=2)
+    torch.cuda.synchronize()
+    for h in range(2):
+        src = kept[0, h].cpu().long()
+        assert torch.equal(k[139000, h, :128].cpu(), new[0][src[:128], h])
+        assert torch.equal(v[5, h, :72].cpu(), new[1][src[128:], h])
+
+
+APPEND = [("fp16", [9, 1, 40], None, 3, 64, 8), ("bf16", [50, 17, 3, 64], [50, 0, 2, 33], 2, 128, 16),
+          ("fp16", [700, 300], [700, 100], 5, 24, 32), ("fp16", [4000], [3999], 8, 128, 64)]
+
+
+@pytest.mark.parametrize("case", APPEND, ids=lambda c: "-".join(map(str, c)).replace(" ", ""))
+def test_append(case):
+    dtype, lens, new, kv, dim, ps = case
+    print(f"[case] append {case}", flush=True)
+    c = Case(dtype, [0] * len(lens), kv, kv, dim, ps, spare=2 + sum(-(-x // ps) for x in lens),
+             max_pages=-(-max(lens) // ps))
+    at = 0
+    for b, x in enumerate(lens):
+        m = -(-x // ps)
+        c.table[b, :m] = torch.tensor(c.free[at:at + m], dtype=torch.int32)
+        at += m
+    c.lens = lens
+    cu = [0]
+    for x in new or [1] * len(lens):
+        cu.append(cu[-1] + x)
+    kn, vn = _randn(c.gen, cu[-1] + 2, kv, dim).to(DT[dtype]), _randn(c.gen, cu[-1] + 2, kv, dim).to(DT[dtype])
+    if new is None:
+        kn, vn = kn[:len(lens)], vn[:len(lens)]
+    k, v, table, ln = c.gpu()
+    G.kv_append(k, v, table, ln, kn.to(DEV), vn.to(DEV),
+                None if new is None else torch.tensor(cu, dtype=torch.int32, device=DEV))
+    for b, n in enumerate(lens):
+        for j in range(cu[b + 1] - cu[b]):
+            t = n - (cu[b + 1] - cu[b]) + j
+            c.k[c.table[b, t // ps], :, t % ps] = kn[cu[b] + j]
+            c.v[c.table[b, t // ps], :, t % ps] = vn[cu[b] + j]
+    assert torch.equal(k.cpu().view(torch.int16), c.k.view(torch.int16))  # new rows there, every other as it was
+    assert torch.equal(v.cpu().view(torch.int16), c.v.view(torch.int16))
+
+
+EVICT = [
+    # dtype, lens, kv heads, dim, page size, budget, sinks, recent, kind of weights
+    ("fp16", [100, 33, 0, 1, 34], 2, 64, 8, 33, 2, 5, "spread"),
+    ("bf16", [1500, 1024, 1025], 3, 128, 16, 1024, 4, 100, "ties"),
+    ("fp16", [300], 1, 80, 32, 1, 0, 0, "spread"),
+    ("fp16", [300, 20], 2, 24, 32, 64, 30, 34, "spread"),   # nothing competes
+    ("fp16", [260], 2, 64, 64, 259, 0, 0, "ties"),
+    ("bf16", [5000], 2, 64, 128, 2000, 1, 1, "odd"),
+    ("fp16", [40], 2, 64, 8, 1000, 2, 3, "spread"),          # a budget beyond the table
+    ("fp16", [3000, 2999], 1, 8, 8, 1500, 0, 0, "zero"),
+    ("fp16", [2500], 1, 64, 16, 1200, 3, 0, "negative"),
+]
+
+
+@pytest.mark.parametrize("case", EVICT, ids=lambda c: "-".join(map(str, c)).replace(" ", ""))
+def test_evict(case):
+    dtype, lens, kv, dim, ps, budget, sinks, recent, kind = case
+    print(f"[case] evict {case}", flush=True)
+    nd = -(-budget // ps)
+    c = Case(dtype, lens, kv, kv, dim, ps, spare=2 + nd * len(lens))
+    into = torch.tensor(c.free[:nd * len(lens)], dtype=torch.int32).view(len(lens), nd)
+    w = c.weights()
+    if kind == "ties":
+        w = (w * 4).floor() / 4
+    elif kind == "zero":
+        w = torch.where(w < 0.5, torch.tensor(0.0), torch.tensor(-0.0))
+    elif kind == "negative":
+        w = w - 0.5
+    elif kind == "odd":
+        w = torch.where(w < 0.1, torch.tensor(float("nan")), torch.where(w < 0.2, torch.tensor(float("inf")), w * 1e-40))
+    k, v, table, ln = c.gpu()
+    t_out, l_out, w_out, kept = G.kv_evict(k, v, table, ln, w.to(DEV), budget, into.to(DEV), sinks=sinks,
+                                           recent=recent)
+    t_out, l_out, w_out, kept = (x.cpu() for x in (t_out, l_out, w_out, kept))
+    for b, n in enumerate(lens):
+        over = n > budget
+        assert int(l_out[b]) == min(n, budget)
+        row = torch.full((c.max_pages,), -1, dtype=torch.int32)
+        row[:nd] = into[b][:c.max_pages]
+        assert torch.equal(t_out[b], row if over else c.table[b])
+        for h in range(kv):
+            take = R.evict_kept(w[b, h].numpy(), n, budget, sinks, recent) if over else list(range(n))
+            assert kept[b, h].tolist() == take + [-1] * (budget - len(take)), (b, h)
+            want = torch.zeros(w.shape[2])
+            want[:len(take)] = w[b, h][take]
+            assert torch.equal(w_out[b, h].view(torch.int32), want.view(torch.int32)) or (
+                torch.equal(torch.nan_to_num(w_out[b, h], 9.0), torch.nan_to_num(want, 9.0)))
+            if over:
+                for i, t in enumerate(take):
+                    c.k[into[b, i // ps], h, i % ps] = c.k[c.table[b, t // ps], h, t % ps]
+                    c.v[into[b, i // ps], h, i % ps] = c.v[c.table[b, t // ps], h, t % ps]
+    assert torch.equal(k.cpu().view(torch.int16), c.k.view(torch.int16))
+    assert torch.equal(v.cpu().view(torch.int16), c.v.view(torch.int16))
