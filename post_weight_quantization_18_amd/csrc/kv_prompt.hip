@@ -4,23 +4,28 @@
 // with t > p - window (or any, window 0) or t < sinks.
 //
 // One pass with a running maximum and sum over tiles of 64 slots. A block takes
-// 128 queries of one head, a wave 32 of them:
-//   S^T [64 slots, 32 queries] = K Q^T,  O^T [dim, 32 queries] += V^T P^T
+// 128 queries of one head, each of its four waves 32 of them, as
+//   S^T [32 slots, 32 queries] = K Q^T,  O^T [dim, 32 queries] += V^T P^T
 // on 32 x 32 matrix instructions. A lane holds one query's column of S^T, so the
 // softmax needs no exchange between lanes but one (the two halves of the
 // column), and only when the running maximum is raised, which waits until a
 // score passes it by 2^8. K rows are assigned to the rows of S^T such that a
 // lane's scores are the P^T operand of the second product as they stand.
-// K is staged in LDS as it is, V turned over (4 x 8 blocks in registers), both
-// padded so that the operand reads meet no bank twice.
-#include <atomic>
-
+//
+// K and V go from memory to LDS by DMA as they lie (a page's rows of a head are
+// contiguous), the next tile while the current one is used, and no registers
+// hold staged data. The chunks of 16 bytes are swizzled on the memory side such
+// that the operand reads meet no bank twice. V's operand needs 8 slots of one
+// element per lane: transpose reads give it. Two blocks share a compute unit:
+// the matrix products of one run beside the softmax of the other.
 #include "kv.h"
 
 namespace gptq {
 namespace {
 
-constexpr int kQ = 128, kT = 64;
+constexpr int kQ = 128;     // queries per block
+constexpr int kT = 64;      // slots per tile
+constexpr int kRing = 2;    // tiles in LDS
 constexpr float kRaise = 8.0f;
 
 // The slots some query of a block sees, as tiles of kT.
@@ -88,282 +93,370 @@ __device__ __forceinline__ int slot_of_row(int m) {
   return 16 * (m >> 4) + 8 * ((m >> 2) & 1) + 4 * ((m >> 3) & 1) + (m & 3);
 }
 
-__device__ __forceinline__ uint32_t finite_only(uint32_t x, uint32_t exp_mask, bool* bad) {
-  // two 16-bit values: one with all exponent bits set is replaced by 0
-  uint32_t lo = (x & exp_mask & 0xffffu) == (exp_mask & 0xffffu) ? 0u : x & 0xffffu;
-  uint32_t hi = (x & exp_mask & 0xffff0000u) == (exp_mask & 0xffff0000u) ? 0u : x & 0xffff0000u;
-  *bad |= (lo | hi) != x;
-  return lo | hi;
+// 16 bytes per lane from base + off (base wave-uniform) to LDS [lds + 16 lane, ...),
+// see dma16 for the M0 handling.
+__device__ __forceinline__ void dma16_from(const void* base, uint32_t off, uint32_t lds) {
+  uint32_t saved;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %1\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %2, %3\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(saved)
+      : "s"(lds), "v"(off), "s"(base)
+      : "memory");
+}
+// Eight rows of K and of V in one go, N transfers each, 1 KB apart in LDS.
+template <int N>
+__device__ __forceinline__ void dma16_octet(const void* kb, const void* vb, const uint32_t (&ok)[N],
+                                            const uint32_t (&ov)[N], uint32_t lds_k, uint32_t lds_v) {
+  uint32_t saved;
+  if constexpr (N == 1) {
+    asm volatile(
+        "s_mov_b32 %0, m0\n\t"
+        "s_mov_b32 m0, %1\n\t"
+        "s_nop 0\n\t"
+        "global_load_lds_dwordx4 %3, %5\n\t"
+        "s_mov_b32 m0, %2\n\t"
+        "s_nop 0\n\t"
+        "global_load_lds_dwordx4 %4, %6\n\t"
+        "s_mov_b32 m0, %0"
+        : "=&s"(saved)
+        : "s"(lds_k), "s"(lds_v), "v"(ok[0]), "v"(ov[0]), "s"(kb), "s"(vb)
+        : "memory");
+  } else {
+    asm volatile(
+        "s_mov_b32 %0, m0\n\t"
+        "s_mov_b32 m0, %1\n\t"
+        "s_nop 0\n\t"
+        "global_load_lds_dwordx4 %5, %9\n\t"
+        "s_mov_b32 m0, %2\n\t"
+        "s_nop 0\n\t"
+        "global_load_lds_dwordx4 %6, %9\n\t"
+        "s_mov_b32 m0, %3\n\t"
+        "s_nop 0\n\t"
+        "global_load_lds_dwordx4 %7, %10\n\t"
+        "s_mov_b32 m0, %4\n\t"
+        "s_nop 0\n\t"
+        "global_load_lds_dwordx4 %8, %10\n\t"
+        "s_mov_b32 m0, %0"
+        : "=&s"(saved)
+        : "s"(lds_k), "s"(lds_k + 1024), "s"(lds_v), "s"(lds_v + 1024), "v"(ok[0]), "v"(ok[1]), "v"(ov[0]), "v"(ov[1]),
+          "s"(kb), "s"(vb)
+        : "memory");
+  }
 }
 
-template <typename T, int DHP>
-struct PromptShared {
-  static constexpr int KP = DHP + 8, VP = kT + 8;  // row pitches, elements
-  T k[2][kT * KP];
-  T v[2][DHP * VP];
-  // by tile modulo 3 (one is read, one written, one cleared), a bit per slot:
-  uint32_t there[3][2];  // lies on a page
-  uint32_t odd[3][2];    // its values hold an infinity or NaN (masked tiles only)
+// The lowest n bits (none below 0, all from 32).
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+// Eight bits for each of the lowest four.
+__device__ __forceinline__ uint32_t octet_bits(uint32_t b) {
+  return ((b & 1) ? 0xffu : 0u) | ((b & 2) ? 0xff00u : 0u) | ((b & 4) ? 0xff0000u : 0u) | ((b & 8) ? 0xff000000u : 0u);
+}
+
+// A wave-uniform value the compiler cannot see to be one, in scalar registers.
+__device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t uni(int64_t x) {
+  return ((int64_t)uni((int)(x >> 32)) << 32) | (uint32_t)uni((int)x);
+}
+
+__device__ __forceinline__ short4v lds_tr(const GPTQ_LDS char* p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((GPTQ_LDS short4v*)p);
+}
+
+// LDS: per tile K then V, kT rows of kPitch bytes.
+template <int QS>
+struct Ring {
+  static constexpr int kPitch = QS <= 4 ? 128 : 256, kLpr = kPitch / 16;  // lanes (16 bytes) per row
+  static constexpr int kHalf = kT * kPitch, kTileBytes = 2 * kHalf, kBytes = kRing * kTileBytes;
+  // where chunk c (16 bytes) of row r lies in its row: c ^ these
+  static constexpr __device__ int fk(int r) { return QS <= 4 ? (r >> 1) & 7 : r & 15; }
+  static constexpr __device__ int fv(int r) { return QS <= 4 ? 4 * ((r >> 1) & 1) : 4 * (r & 3); }
 };
 
-// LSE: the row's log2 of the sum of 2^score goes to lse [n_tokens][n_heads].
-template <typename T, int DHP, bool LSE>
+// QS: steps of 16 along the head for the scores (16 QS >= dim). LSE: the row's
+// log2 of the sum of 2^score goes to lse [n_tokens][n_heads].
+template <typename T, int QS, bool LSE>
 __global__ __launch_bounds__(256, 2) void prompt_kernel(KvView c, KvAttnArgs a, const int32_t* cu, int n_rows,
                                                         int n_blk, float* lse) {
   using KT = KvType<T>;
   using x8 = typename KT::x8;
-  using Sh = PromptShared<T, DHP>;
-  constexpr int CH = DHP / 8, NK = kT * CH / 256, QS = DHP / 16, NO = DHP / 32;
-  constexpr uint32_t kExp = __is_same(T, half_t) ? 0x7c007c00u : 0x7f807f80u;
-  extern __shared__ __attribute__((aligned(16))) char smem[];
-  Sh& sh = *(Sh*)smem;
+  using R = Ring<QS>;
+  constexpr int NO = (QS + 1) / 2;
+  constexpr int kRows = 64 / R::kLpr, kDma = 8 / kRows;  // rows per transfer, transfers per octet
+  constexpr uint32_t kExp = __is_same(T, half_t) ? 0x7c00u : 0x7f80u;
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  __shared__ uint32_t odd[4][2];  // by tile modulo 4, a bit per slot: its values hold an infinity or NaN
+  const GPTQ_LDS char* lds = (const GPTQ_LDS char*)smem;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
   const int id = xcd_logical_block(blockIdx.x, gridDim.x);
   const int h = id / n_blk;
   const Where at(cu, c.n_seqs, n_blk - 1 - (id - h * n_blk), n_rows);  // late queries see most: first
   if (at.b < 0) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
   const int col = lane & 31, half = lane >> 5;
   const int kvh = h / (a.n_heads / c.n_kv);
-  const int len = c.len(at.b);
-  const int p0 = len - at.n_b + at.i0;                                   // position of the block's first query
-  const int rows = at.n_b - at.i0 < kQ ? at.n_b - at.i0 : kQ;            // its queries
+  const int len = uni(c.len(at.b));
+  const int p0 = len - at.n_b + at.i0;                         // position of the block's first query
+  const int rows = at.n_b - at.i0 < kQ ? at.n_b - at.i0 : kQ;  // its queries
   const int first = a.window > 0 && p0 - a.window + 1 > 0 ? p0 - a.window + 1 : 0;
   const int end = p0 + rows > 0 ? p0 + rows : 0;
-  const Tiles tl(end, first < end ? first : end, a.sinks);
+  Tiles tl(end, first < end ? first : end, a.sinks);
+  tl.n = uni(tl.n);
+  tl.sink_tiles = uni(tl.sink_tiles);
+  tl.jump = uni(tl.jump);
+  tl.total = uni(tl.total);
   const int32_t* table = c.table + (int64_t)at.b * c.ld_table;
   const int chunks = c.dim >> 3;
 
+  // a negative scale is the queries' sign; a zero one is next to it (equal weights either way)
+  const float sc = fmaxf(__builtin_fabsf(a.scale) * kLog2e, 1e-30f), raise = kRaise / sc;
+  const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
   const int qi = wave * 32 + col, pos = p0 + qi;  // this lane's query
-  const bool q_ok = qi < rows;
   x8 q[QS];
   {
-    const T* qp = (const T*)a.q + (int64_t)(at.row0 + at.i0 + (q_ok ? qi : 0)) * a.ldq + (int64_t)h * c.dim;
+    const T* qp = (const T*)a.q + (int64_t)(at.row0 + at.i0 + (qi < rows ? qi : 0)) * a.ldq + (int64_t)h * c.dim;
 #pragma unroll
     for (int i = 0; i < QS; ++i) {
       const int ch = 2 * i + half;
       const bool ok = ch < chunks;
-      const uint4v z = *(const uint4v*)(qp + 8 * (ok ? ch : 0));
+      const uint4v z = *(const uint4v*)(qp + 8 * (ok ? ch : 0)) ^ (uint4v){flip, flip, flip, flip};
       q[i] = __builtin_bit_cast(x8, (uint4v){ok ? z[0] : 0u, ok ? z[1] : 0u, ok ? z[2] : 0u, ok ? z[3] : 0u});
     }
   }
-  const float sc = a.scale * kLog2e;
   float16v o[NO];
 #pragma unroll
   for (int i = 0; i < NO; ++i) o[i] = (float16v){0};
-  float m = -INFINITY, lsum = 0.0f;
+  float m = -INFINITY, lsum = 0.0f;  // largest score seen, before the scale; sum of this lane's weights
 
-  // this wave's queries: positions w0 .. w1
+  // Tile numbers. Those before sink_tiles are always gone through slot by slot; behind them
+  // this wave (queries at w0 .. w1) sees something of the tiles [vis_lo, vis_hi) (and of
+  // earlier ones that still hold sinks), and every
+  // slot of [full_lo, full_hi); every query of the block sees all of [all_lo, all_hi).
   const int w0 = p0 + wave * 32, w1 = w0 + 31 < end - 1 ? w0 + 31 : end - 1;
+  const int to_s = tl.sink_tiles - tl.jump;  // tile number of slot 0, were there no gap
+  const int full_hi = to_s + ((w0 - kT + 1) >> 6) + 1, all_hi = to_s + ((p0 - kT + 1) >> 6) + 1;
+  int full_lo = tl.sink_tiles, all_lo = tl.sink_tiles, vis_lo = 0, vis_hi = to_s + (w1 >> 6) + 1;
+  if (a.window > 0) {
+    const int lo = to_s + ((w1 - a.window) >> 6) + 1, alo = to_s + ((p0 + rows - 1 - a.window) >> 6) + 1;
+    if (lo > full_lo) full_lo = lo;
+    if (alo > all_lo) all_lo = alo;
+    vis_lo = to_s + ((w0 - a.window - kT + 1) >> 6) + 1;
+  }
+  const bool idle = w0 >= end || w1 < 0;  // a wave without queries, or whose queries stand before slot 0
+  auto hidden = [&](int s) __attribute__((always_inline)) {
+    return idle || (s >= tl.sink_tiles && ((s < vis_lo && tl.slot0(s) >= a.sinks) || s >= vis_hi));
+  };
 
+  // this wave's 16 rows of every tile: two octets
+  const int lrow = lane / R::kLpr, lpos = lane % R::kLpr;
+  uint32_t off_k[2][kDma], off_v[kDma];
+  bool has_k[2][kDma], has_v;
+#pragma unroll
+  for (int i = 0; i < kDma; ++i) {
+#pragma unroll
+    for (int oc = 0; oc < 2; ++oc) {
+      const int r = 8 * oc + kRows * i + lrow, ch = lpos ^ R::fk(r);
+      has_k[oc][i] = ch < chunks;
+      off_k[oc][i] = ((r & 7) * c.dim + (ch < chunks ? ch : 0) * 8) * 2;
+    }
+    const int ch = lpos ^ R::fv(lrow);
+    has_v = ch < chunks;
+    off_v[i] = ((kRows * i + lrow) * c.dim + (ch < chunks ? ch : 0) * 8) * 2;
+  }
+  // dim = 16 QS: no product reads a chunk behind the head's end, and what lands there is not
+  // looked at. Otherwise these chunks stay as they are cleared below.
+  const bool exact = c.dim == 16 * QS;
   const T* kb = (const T*)c.k + (int64_t)kvh * c.page_size * c.dim;
   const T* vb = (const T*)c.v + (int64_t)kvh * c.page_size * c.dim;
-  const int vquad = tid & 15, vchunk = tid >> 4;  // V: 4 slots x 8 elements
-  struct Pages {
-    int k[NK], v;
+  // pages of the octets of eight tiles, one per lane
+  auto pages = [&](int s8) __attribute__((always_inline)) {
+    const int s = 8 * s8 + (lane >> 3), t = tl.slot0(s) + 8 * (lane & 7);
+    return s < tl.total && t < tl.n ? table[t >> c.page_shift] : -1;
   };
-  auto pages = [&](int s) __attribute__((always_inline)) {
-    Pages p;
-    const int t0 = tl.slot0(s);
+  auto stage = [&](int s, int pg) __attribute__((always_inline)) {
+    const uint32_t to = lds0 + (s & 1) * R::kTileBytes + 16 * wave * R::kPitch;
+    const int row0 = tl.slot0(s) + 16 * wave;
 #pragma unroll
-    for (int i = 0; i < NK; ++i) {
-      const int t = t0 + (tid + 256 * i) / CH;
-      p.k[i] = s < tl.total && t < tl.n ? table[t >> c.page_shift] : -1;
-    }
-    const int t = t0 + 4 * vquad;
-    p.v = s < tl.total && t < tl.n ? table[t >> c.page_shift] : -1;
-    return p;
-  };
-  struct Stage {
-    uint4v k[NK], v[4];
-  };
-  auto load = [&](int s, const Pages& p, Stage& r) __attribute__((always_inline)) {
-    const int t0 = tl.slot0(s);
+    for (int oc = 0; oc < 2; ++oc) {
+      const int p = __builtin_amdgcn_readlane(pg, 8 * (s & 7) + 2 * wave + oc);
+      const uint32_t to_oc = to + 8 * oc * R::kPitch;
+      if ((uint32_t)p < (uint32_t)c.n_pages) {
+        const int64_t from = uni((int64_t)p * c.page_stride + ((row0 + 8 * oc) & (c.page_size - 1)) * c.dim);
+        if (exact) {
+          dma16_octet<kDma>(kb + from, vb + from, off_k[oc], off_v, to_oc, to_oc + R::kHalf);
+        } else {
 #pragma unroll
-    for (int i = 0; i < NK; ++i) {
-      const int it = tid + 256 * i, row = it / CH, ch = it - row * CH;
-      r.k[i] = (uint4v){0, 0, 0, 0};
-      if (c.page_ok(p.k[i]) && ch < chunks)
-        r.k[i] = *(const uint4v*)(kb + (int64_t)p.k[i] * c.page_stride + ((t0 + row) & (c.page_size - 1)) * c.dim + ch * 8);
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      r.v[j] = (uint4v){0, 0, 0, 0};
-      const int t = t0 + 4 * vquad + j;
-      if (c.page_ok(p.v) && t < tl.n && vchunk < chunks)
-        r.v[j] = *(const uint4v*)(vb + (int64_t)p.v * c.page_stride + (t & (c.page_size - 1)) * c.dim + vchunk * 8);
-    }
-  };
-  // whether every query of the block sees every slot of tile s
-  auto whole = [&](int s) __attribute__((always_inline)) {
-    const int t0 = tl.slot0(s), t1 = t0 + kT - 1;
-    const int low = a.window > 0 ? p0 + rows - 1 - a.window + 1 : 0;  // first slot of the last query's window
-    return t1 <= p0 && (t0 >= low || t1 < a.sinks);
-  };
-  auto store = [&](int s, int buf, int bits, const Pages& p, Stage& r) __attribute__((always_inline)) {
-    const bool masked = !whole(s);
-#pragma unroll
-    for (int i = 0; i < NK; ++i) {
-      const int it = tid + 256 * i, row = it / CH, ch = it - row * CH;
-      *(uint4v*)&sh.k[buf][row * Sh::KP + ch * 8] = r.k[i];
-    }
-    if (vchunk == 0 && !c.page_ok(p.v)) {
-      const int t = 4 * vquad;
-      atomicAnd(&sh.there[bits][t >> 5], ~(0xfu << (t & 31)));
-    }
-    if (masked) {
-      // a value that is not finite must not reach the queries that do not see its slot
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        bool bad = false;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) r.v[j][e] = finite_only(r.v[j][e], kExp, &bad);
-        const int t = 4 * vquad + j;
-        if (bad) atomicOr(&sh.odd[bits][t >> 5], 1u << (t & 31));
-      }
-    }
-    if (vchunk < CH) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t sel = (e & 1) ? 0x07060302u : 0x05040100u;
-        uint2v x;
-        x[0] = __builtin_amdgcn_perm(r.v[1][e / 2], r.v[0][e / 2], sel);
-        x[1] = __builtin_amdgcn_perm(r.v[3][e / 2], r.v[2][e / 2], sel);
-        *(uint2v*)&sh.v[buf][(vchunk * 8 + e) * Sh::VP + 4 * vquad] = x;
+          for (int i = 0; i < kDma; ++i) {
+            if (has_k[oc][i]) dma16_from(kb + from, off_k[oc][i], to_oc + 1024 * i);
+            if (has_v) dma16_from(vb + from, off_v[i], to_oc + 1024 * i + R::kHalf);
+          }
+        }
+      } else {
+        // no such slots: nothing may reach the second product from here
+        for (int i = 0; i < kDma; ++i)
+          *(GPTQ_LDS uint4v*)(lds + (to_oc - lds0) + 1024 * i + R::kHalf + 16 * lane) = (uint4v){0, 0, 0, 0};
       }
     }
   };
-  auto clear = [&](int bits) __attribute__((always_inline)) {
-    if (tid < 2) {
-      sh.there[bits][tid] = ~0u;
-      sh.odd[bits][tid] = 0u;
+  // In a tile that is hidden in part from some query, a value that is not finite must not
+  // reach the queries that do not see its slot (0 x NaN): each wave looks through its own
+  // rows, replaces these by 0 and notes the slots; the queries that see them get them
+  // afterwards.
+  auto clean = [&](int s) __attribute__((always_inline)) {
+    const int t0 = tl.slot0(s);
+    GPTQ_LDS char* v = (GPTQ_LDS char*)lds + (s & 1) * R::kTileBytes + R::kHalf + 16 * wave * R::kPitch;
+    for (int i = 0; i < 2 * kDma; ++i) {
+      GPTQ_LDS uint4v* at_v = (GPTQ_LDS uint4v*)(v + 1024 * i + 16 * lane);
+      if (!has_v) continue;
+      const uint4v x = *at_v;
+      uint4v y;
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t lo = (x[e] & kExp) == kExp ? 0u : x[e] & 0xffffu;
+        const uint32_t hi = ((x[e] >> 16) & kExp) == kExp ? 0u : x[e] & 0xffff0000u;
+        y[e] = lo | hi;
+      }
+      if (y[0] != x[0] || y[1] != x[1] || y[2] != x[2] || y[3] != x[3]) {
+        *at_v = y;
+        const int k = 16 * wave + kRows * i + lrow;
+        if (t0 + k < tl.n) atomicOr(&odd[s & 3][k >> 5], 1u << (k & 31));
+      }
     }
   };
-  auto sees = [&](int t) __attribute__((always_inline)) {
-    return t <= pos && (a.window <= 0 || t > pos - a.window || t < a.sinks);
+  // bit k: this lane's query sees slot t0 + k
+  auto seen = [&](int t0) __attribute__((always_inline)) {
+    uint32_t see = low_bits(pos + 1 - t0);
+    if (a.window > 0) see &= ~low_bits(pos + 1 - a.window - t0) | low_bits(a.sinks - t0);
+    return see;
   };
 
-  auto compute = [&](int s, int buf, int bits) __attribute__((always_inline)) {
-    const int t0 = tl.slot0(s);
-    const bool off_page = (sh.there[bits][0] & sh.there[bits][1]) != ~0u;
-    // nothing of this tile for any query of this wave
-    if (t0 > w1 || w0 >= end || w1 < 0) return;
-    if (a.window > 0 && t0 + kT - 1 <= w0 - a.window && t0 >= a.sinks) return;
-    float16v sv[2];
+  // operand addresses within a tile
+  const int krow = slot_of_row(col);
+  uint32_t at_k[QS], at_v[NO];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      sv[u] = (float16v){0};
-      const T* kp = &sh.k[buf][(32 * u + slot_of_row(col)) * Sh::KP + 8 * half];
+  for (int i = 0; i < QS; ++i) at_k[i] = krow * R::kPitch + (((2 * i + half) ^ R::fk(krow)) * 16);
+  {
+    const int j = lane & 15, r = 8 * half + (j >> 2);
 #pragma unroll
-      for (int i = 0; i < QS; ++i) sv[u] = KT::mfma32(*(const x8*)(kp + 16 * i), q[i], sv[u]);
+    for (int i = 0; i < NO; ++i)
+      at_v[i] = R::kHalf + r * R::kPitch + (((4 * i + 2 * ((lane >> 4) & 1) + ((j & 3) >> 1)) ^ R::fv(r)) * 16) + 8 * (j & 1);
+  }
+  // scores of the 32 slots u of a tile
+  auto scores = [&](const GPTQ_LDS char* b, int u) __attribute__((always_inline)) {
+    float16v x = (float16v){0};
+#pragma unroll
+    for (int i = 0; i < QS; ++i) x = KT::mfma32(*(const GPTQ_LDS x8*)(b + at_k[i] + 32 * u * R::kPitch), q[i], x);
+    return x;
+  };
+  auto mask = [&](float16v& x, int t0, uint32_t page_bits) __attribute__((always_inline)) {
+    const uint32_t see = (seen(t0) & page_bits) >> (8 * half);
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const uint32_t keep = (uint32_t)((int)(see << (31 - 16 * (r >> 3) - (r & 7))) >> 31);
+      const float v = x[r];  // (a bit cast of the vector's element itself would take element 0)
+      x[r] = __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, v) & keep) | (0xff800000u & ~keep));
     }
-    const bool all = !off_page && t0 + kT - 1 <= w0 && (a.window <= 0 || t0 > w1 - a.window || t0 + kT <= a.sinks);
+  };
+  auto softmax = [&](const float16v& x, float base, x8(&pf)[2]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int r = 0; r < 16; ++r) {
+      const float p = __builtin_amdgcn_exp2f(fmaf(x[r], sc, -base));
+      lsum += p;
+      // P in the cache's type: its rounding (2^-11 or 2^-8 of each weight at most) averages
+      // out over the slots and stays below that of the output
+      pf[r >> 3][r & 7] = (T)p;
+    }
+  };
+  auto values = [&](const GPTQ_LDS char* b, int u, const x8(&pf)[2]) __attribute__((always_inline)) {
 #pragma unroll
-      for (int r = 0; r < 16; ++r) sv[u][r] *= sc;
-    if (!all) {
+    for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const uint32_t there = sh.there[bits][u];
+      for (int i = 0; i < NO; ++i) {
+        const GPTQ_LDS char* p = b + at_v[i] + (32 * u + 16 * k) * R::kPitch;
+        const short4v lo = lds_tr(p), hi = lds_tr(p + 4 * R::kPitch);
+        o[i] = KT::mfma32(__builtin_bit_cast(x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7)), pf[k], o[i]);
+      }
+  };
+  // rare: values of a tile that are not finite, for the queries that see them (their weight is
+  // positive, so the sum is what the value is)
+  auto add_odd = [&](int t0, uint32_t bits) __attribute__((always_inline)) {
+    const uint32_t see = seen(t0);
+    for (int k = 0; k < 32; ++k) {
+      if (!((bits >> k) & 1)) continue;
+      const int t = t0 + k, pg = table[t >> c.page_shift];
+      if (!c.page_ok(pg)) continue;
+      const T* vp = vb + (int64_t)pg * c.page_stride + (int64_t)(t & (c.page_size - 1)) * c.dim + 4 * half;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int k = 16 * (r >> 3) + 8 * half + (r & 7), t = t0 + 32 * u + k;
-          sv[u][r] = sees(t) && ((there >> k) & 1) ? sv[u][r] : -INFINITY;
+      for (int i = 0; i < NO; ++i)
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4) {
+          typedef T x4 __attribute__((ext_vector_type(4)));
+          x4 z = (x4){0, 0, 0, 0};
+          if (32 * i + 8 * r4 < c.dim) z = *(const x4*)(vp + 32 * i + 8 * r4);
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            o[i][4 * r4 + r] += ((see >> k) & 1) && !(__builtin_fabsf((float)z[r]) < INFINITY) ? (float)z[r] : 0.0f;
+          asm volatile("" ::: "memory");  // one load at a time: no registers for more
         }
-      }
-    }
-    float top = -INFINITY;
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) top = fmaxf(top, sv[u][r]);
-    if (__any(top > m + kRaise)) {
-      top = fmaxf(top, __shfl_xor(top, 32));
-      const float nm = fmaxf(m, top);
-      const float f = m == -INFINITY ? 0.0f : exp2f(m - nm);
-      m = nm;
-      lsum *= f;
-#pragma unroll
-      for (int i = 0; i < NO; ++i) o[i] *= f;
-    }
-    const float base = m == -INFINITY ? 0.0f : m;
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        sv[u][r] = __builtin_amdgcn_exp2f(sv[u][r] - base);
-        lsum += sv[u][r];
-      }
-    // P in the cache's type: its rounding (2^-12 or 2^-9 of each weight at most) averages out
-    // over the slots and stays below that of the output
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        x8 pf;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) pf[j] = (T)sv[u][8 * k + j];
-#pragma unroll
-        for (int i = 0; i < NO; ++i) {
-          const x8 va = *(const x8*)&sh.v[buf][(32 * i + col) * Sh::VP + 32 * u + 16 * k + 8 * half];
-          o[i] = KT::mfma32(va, pf, o[i]);
-        }
-      }
-    if ((sh.odd[bits][0] | sh.odd[bits][1]) != 0u) {
-      // rare: the values that are not finite, for the queries that see them
-      for (int k = 0; k < kT; ++k) {
-        if (!((sh.odd[bits][k >> 5] >> (k & 31)) & 1)) continue;
-        float pk = 0.0f;
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int r = 0; r < 16; ++r)
-            if (32 * u + 16 * (r >> 3) + 8 * half + (r & 7) == k) pk = sv[u][r];
-        const float other = __shfl_xor(pk, 32);
-        if (((k >> 3) & 1) != half) pk = other;
-        if (!sees(t0 + k)) continue;
-        const int t = t0 + k, pg = table[t >> c.page_shift];
-        if (!c.page_ok(pg)) continue;
-        const T* vp = vb + (int64_t)pg * c.page_stride + (t & (c.page_size - 1)) * c.dim;
-#pragma unroll
-        for (int i = 0; i < NO; ++i)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int e = 32 * i + 8 * (r >> 2) + 4 * half + (r & 3);
-            if (e >= c.dim) continue;
-            const float x = (float)vp[e];
-            if (!(__builtin_fabsf(x) < INFINITY)) o[i][r] += pk * x;
-          }
-      }
     }
   };
 
   if (tl.total > 0) {
-    Stage st;
-    Pages pa = pages(0);
-    clear(0);
-    clear(1);
-    load(0, pa, st);
-    Pages pb = pages(1);
+    if (tid < 8) odd[tid >> 1][tid & 1] = 0u;
+    if (!exact)
+      for (int i = tid; i < R::kBytes / 16; i += 256) *(GPTQ_LDS uint4v*)(lds + 16 * i) = (uint4v){0, 0, 0, 0};
+    int pg = pages(0), pg_next = pages(1);
     __syncthreads();
-    store(0, 0, 0, pa, st);
-    __syncthreads();
-    int bits = 0;  // s modulo 3
+    stage(0, pg);
     for (int s = 0; s < tl.total; ++s) {
-      const int buf = s & 1, next = bits == 2 ? 0 : bits + 1;
-      if (s + 1 < tl.total) load(s + 1, pb, st);
-      pa = pb;
-      pb = pages(s + 2);
-      clear(next == 2 ? 0 : next + 1);  // tile s + 2's, read last by tile s - 1
-      compute(s, buf, bits);
-      if (s + 1 < tl.total) store(s + 1, buf ^ 1, next, pa, st);
-      __syncthreads();
-      bits = next;
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");  // this wave's rows of tile s have landed
+      const bool in_part = s < all_lo || s >= all_hi;
+      if (in_part) clean(s);
+      if (tid < 2) odd[(s + 2) & 3][tid] = 0u;  // read last by tile s - 2, written next two barriers from here
+      lds_barrier();  // tile s is in LDS for every wave, tile s - 1 is read by none
+      const uint64_t good = __ballot(c.page_ok(pg));
+      const uint32_t on_page = (uint32_t)(good >> (8 * (s & 7))) & 0xffu;
+      if ((s & 7) == 7) {
+        pg = pg_next;
+        pg_next = pages((s >> 3) + 2);
+      }
+      if (s + 1 < tl.total) stage(s + 1, pg);
+      if (hidden(s)) continue;
+      const GPTQ_LDS char* b = lds + (s & 1) * R::kTileBytes;
+      const int t0 = tl.slot0(s);
+      float16v x = scores(b, 0), y = scores(b, 1);
+      if (s < full_lo || s >= full_hi || on_page != 0xffu) {
+        mask(x, t0, octet_bits(on_page));
+        mask(y, t0 + 32, octet_bits(on_page >> 4));
+      }
+      float top = fmaxf(x[0], y[0]);
+#pragma unroll
+      for (int r = 1; r < 16; ++r) top = fmaxf(top, fmaxf(x[r], y[r]));
+      if (__any(top > m + raise)) {
+        const float nm = fmaxf(m, fmaxf(top, __shfl_xor(top, 32)));
+        const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m - nm) * sc);
+        m = nm;
+        lsum *= f;
+#pragma unroll
+        for (int i = 0; i < NO; ++i) o[i] *= f;
+      }
+      const float base = m == -INFINITY ? 0.0f : m * sc;
+      x8 px[2], py[2];
+      softmax(x, base, px);
+      values(b, 0, px);
+      softmax(y, base, py);
+      values(b, 1, py);
+      if (in_part) {
+        const uint32_t o0 = uni((int)odd[s & 3][0]), o1 = uni((int)odd[s & 3][1]);
+        if (o0) add_odd(t0, o0);
+        if (o1) add_odd(t0 + 32, o1);
+      }
     }
   }
 
   lsum += __shfl_xor(lsum, 32);
-  if (!q_ok) return;
+  if (qi >= rows) return;
   const float inv = lsum == 0.0f ? 0.0f : 1.0f / lsum;
   const int64_t row = at.row0 + at.i0 + qi;
   T* op = (T*)a.out + row * a.ldo + (int64_t)h * c.dim;
@@ -374,15 +467,16 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(KvView c, KvAttnArgs a, 
       const int e = 32 * i + 8 * r4 + 4 * half;
       if (e < c.dim) {
         typedef T x4 __attribute__((ext_vector_type(4)));
-        x4 y;
+        x4 z;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) y[r] = lsum == 0.0f ? (T)0.0f : (T)(o[i][4 * r4 + r] * inv);
-        *(x4*)(op + e) = y;
+        for (int r = 0; r < 4; ++r) z[r] = lsum == 0.0f ? (T)0.0f : (T)(o[i][4 * r4 + r] * inv);
+        *(x4*)(op + e) = z;
       }
     }
   if constexpr (LSE) {
     // a row without a weight: +infinity, so that 2^(score - lse) is 0
-    if (half == 0) lse[row * a.n_heads + h] = lsum == 0.0f ? INFINITY : m + log2f(lsum);
+    if (half == 0)
+      lse[row * a.n_heads + h] = lsum == 0.0f ? INFINITY : (m == -INFINITY ? 0.0f : m * sc) + log2f(lsum);
   }
 }
 
@@ -482,46 +576,41 @@ __global__ __launch_bounds__(256, 2) void prompt_weights_kernel(KvView c, KvAttn
   }
 }
 
-template <typename T, int DHP>
-gptq_status_t launch(const KvView& c, const KvAttnArgs& a, const int32_t* cu, int64_t n_tokens, float* lse,
-                     hipStream_t st) {
+template <typename T, int QS, bool LSE>
+gptq_status_t launch_rows(const KvView& c, const KvAttnArgs& a, const int32_t* cu, int64_t n_tokens, float* lse,
+                          hipStream_t st) {
   const int64_t n_blk = n_tokens / kQ + c.n_seqs;  // at least the ragged batch's blocks
   const int64_t blocks = n_blk * a.n_heads;
-  const int64_t cap = (int64_t)c.max_pages << c.page_shift, n_tiles = ceil_div(cap, 128);
-  const int64_t wblocks = n_tiles * c.n_kv * c.n_seqs;
-  if (blocks * 256 >= (int64_t)1 << 32 || wblocks * 256 >= (int64_t)1 << 32) return GPTQ_ERR_UNSUPPORTED;
-  const size_t lds = sizeof(PromptShared<T, DHP>);
-  const void* fn = a.weights ? (const void*)prompt_kernel<T, DHP, true> : (const void*)prompt_kernel<T, DHP, false>;
-  // more than 64 KB of LDS has to be asked for, once per device and kernel
-  static std::atomic<uint64_t> asked[2];
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess) return GPTQ_ERR_HIP;
-  std::atomic<uint64_t>& flags = asked[a.weights ? 1 : 0];
-  if (!((flags.load(std::memory_order_acquire) >> dev) & 1)) {
-    if (hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) != hipSuccess) return GPTQ_ERR_HIP;
-    flags.fetch_or(1ull << dev, std::memory_order_release);
-  }
-  if (a.weights)
-    hipLaunchKernelGGL((prompt_kernel<T, DHP, true>), dim3((unsigned)blocks), dim3(256), lds, st, c, a, cu,
-                       (int)n_tokens, (int)n_blk, lse);
-  else
-    hipLaunchKernelGGL((prompt_kernel<T, DHP, false>), dim3((unsigned)blocks), dim3(256), lds, st, c, a, cu,
-                       (int)n_tokens, (int)n_blk, lse);
+  if (blocks * 256 >= (int64_t)1 << 32) return GPTQ_ERR_UNSUPPORTED;
+  hipLaunchKernelGGL((prompt_kernel<T, QS, LSE>), dim3((unsigned)blocks), dim3(256), Ring<QS>::kBytes, st, c, a, cu,
+                     (int)n_tokens, (int)n_blk, lse);
   GPTQ_CHECK_LAUNCH();
-  if (a.weights) {
-    hipLaunchKernelGGL((prompt_weights_kernel<T, DHP>), dim3((unsigned)wblocks), dim3(256), 0, st, c, a, cu,
-                       (int)n_tokens, (int)n_tiles, lse);
-    GPTQ_CHECK_LAUNCH();
-  }
   return GPTQ_OK;
 }
 
+template <typename T, int QS>
+gptq_status_t launch(const KvView& c, const KvAttnArgs& a, const int32_t* cu, int64_t n_tokens, float* lse,
+                     hipStream_t st) {
+  const int64_t cap = (int64_t)c.max_pages << c.page_shift, n_tiles = ceil_div(cap, 128);
+  const int64_t wblocks = n_tiles * c.n_kv * c.n_seqs;
+  if (wblocks * 256 >= (int64_t)1 << 32) return GPTQ_ERR_UNSUPPORTED;
+  const gptq_status_t rc = a.weights ? launch_rows<T, QS, true>(c, a, cu, n_tokens, lse, st)
+                                     : launch_rows<T, QS, false>(c, a, cu, n_tokens, lse, st);
+  if (rc != GPTQ_OK || !a.weights) return rc;
+  hipLaunchKernelGGL((prompt_weights_kernel<T, 16 * QS>), dim3((unsigned)wblocks), dim3(256), 0, st, c, a, cu,
+                     (int)n_tokens, (int)n_tiles, lse);
+  GPTQ_CHECK_LAUNCH();
+  return GPTQ_OK;
+}
+
+// Steps along the head: 5 is OPT-2.7B's head of 80, which 6 would slow by a sixth.
 template <typename T>
 gptq_status_t prompt_enqueue(const KvView& c, const KvAttnArgs& a, const int32_t* cu, int64_t n_tokens, float* lse,
                              hipStream_t st) {
-  if (c.dim <= 64) return launch<T, 64>(c, a, cu, n_tokens, lse, st);
-  if (c.dim <= 96) return launch<T, 96>(c, a, cu, n_tokens, lse, st);
-  return launch<T, 128>(c, a, cu, n_tokens, lse, st);
+  if (c.dim <= 64) return launch<T, 4>(c, a, cu, n_tokens, lse, st);
+  if (c.dim <= 80) return launch<T, 5>(c, a, cu, n_tokens, lse, st);
+  if (c.dim <= 96) return launch<T, 6>(c, a, cu, n_tokens, lse, st);
+  return launch<T, 8>(c, a, cu, n_tokens, lse, st);
 }
 
 }  // namespace
