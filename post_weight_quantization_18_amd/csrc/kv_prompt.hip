@@ -232,15 +232,14 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(KvView c, KvAttnArgs a, 
 
   // Tile numbers. Those before sink_tiles are always gone through slot by slot; behind them
   // this wave (queries at w0 .. w1) sees something of the tiles [vis_lo, vis_hi) (and of
-  // earlier ones that still hold sinks), and every
-  // slot of [full_lo, full_hi); every query of the block sees all of [all_lo, all_hi).
+  // earlier ones that still hold sinks); every query
+  // of the block sees all of [all_lo, all_hi).
   const int w0 = p0 + wave * 32, w1 = w0 + 31 < end - 1 ? w0 + 31 : end - 1;
   const int to_s = tl.sink_tiles - tl.jump;  // tile number of slot 0, were there no gap
-  const int full_hi = to_s + ((w0 - kT + 1) >> 6) + 1, all_hi = to_s + ((p0 - kT + 1) >> 6) + 1;
-  int full_lo = tl.sink_tiles, all_lo = tl.sink_tiles, vis_lo = 0, vis_hi = to_s + (w1 >> 6) + 1;
+  const int all_hi = to_s + ((p0 - kT + 1) >> 6) + 1;
+  int all_lo = tl.sink_tiles, vis_lo = 0, vis_hi = to_s + (w1 >> 6) + 1;
   if (a.window > 0) {
-    const int lo = to_s + ((w1 - a.window) >> 6) + 1, alo = to_s + ((p0 + rows - 1 - a.window) >> 6) + 1;
-    if (lo > full_lo) full_lo = lo;
+    const int alo = to_s + ((p0 + rows - 1 - a.window) >> 6) + 1;
     if (alo > all_lo) all_lo = alo;
     vis_lo = to_s + ((w0 - a.window - kT + 1) >> 6) + 1;
   }
@@ -252,17 +251,14 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(KvView c, KvAttnArgs a, 
   // this wave's 16 rows of every tile: two octets
   const int lrow = lane / R::kLpr, lpos = lane % R::kLpr;
   uint32_t off_k[2][kDma], off_v[kDma];
-  bool has_k[2][kDma], has_v;
 #pragma unroll
   for (int i = 0; i < kDma; ++i) {
 #pragma unroll
     for (int oc = 0; oc < 2; ++oc) {
       const int r = 8 * oc + kRows * i + lrow, ch = lpos ^ R::fk(r);
-      has_k[oc][i] = ch < chunks;
       off_k[oc][i] = ((r & 7) * c.dim + (ch < chunks ? ch : 0) * 8) * 2;
     }
     const int ch = lpos ^ R::fv(lrow);
-    has_v = ch < chunks;
     off_v[i] = ((kRows * i + lrow) * c.dim + (ch < chunks ? ch : 0) * 8) * 2;
   }
   // dim = 16 QS: no product reads a chunk behind the head's end, and what lands there is not
@@ -287,10 +283,12 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(KvView c, KvAttnArgs a, 
         if (exact) {
           dma16_octet<kDma>(kb + from, vb + from, off_k[oc], off_v, to_oc, to_oc + R::kHalf);
         } else {
+          int lp = lpos;
+          asm volatile("" : "+v"(lp));
 #pragma unroll
           for (int i = 0; i < kDma; ++i) {
-            if (has_k[oc][i]) dma16_from(kb + from, off_k[oc][i], to_oc + 1024 * i);
-            if (has_v) dma16_from(vb + from, off_v[i], to_oc + 1024 * i + R::kHalf);
+            if ((lp ^ R::fk(8 * oc + kRows * i + lrow)) < chunks) dma16_from(kb + from, off_k[oc][i], to_oc + 1024 * i);
+            if ((lp ^ R::fv(lrow)) < chunks) dma16_from(vb + from, off_v[i], to_oc + 1024 * i + R::kHalf);
           }
         }
       } else {
@@ -306,10 +304,21 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(KvView c, KvAttnArgs a, 
   // afterwards.
   auto clean = [&](int s) __attribute__((always_inline)) {
     const int t0 = tl.slot0(s);
-    GPTQ_LDS char* v = (GPTQ_LDS char*)lds + (s & 1) * R::kTileBytes + R::kHalf + 16 * wave * R::kPitch;
+    GPTQ_LDS char* v = (GPTQ_LDS char*)lds + (s & 1) * R::kTileBytes + R::kHalf + 16 * wave * R::kPitch + 16 * lane;
+    typedef unsigned short u2 __attribute__((ext_vector_type(2)));
+    u2 most = (u2){0, 0};  // largest magnitude, as bits
+#pragma unroll
     for (int i = 0; i < 2 * kDma; ++i) {
-      GPTQ_LDS uint4v* at_v = (GPTQ_LDS uint4v*)(v + 1024 * i + 16 * lane);
-      if (!has_v) continue;
+      const uint4v x = *(GPTQ_LDS uint4v*)(v + 1024 * i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t w = x[e] & 0x7fff7fffu;
+        most = __builtin_elementwise_max(most, __builtin_bit_cast(u2, w));
+      }
+    }
+    if (!__any(most[0] >= kExp || most[1] >= kExp)) return;
+    for (int i = 0; i < 2 * kDma; ++i) {
+      GPTQ_LDS uint4v* at_v = (GPTQ_LDS uint4v*)(v + 1024 * i);
       const uint4v x = *at_v;
       uint4v y;
       for (int e = 0; e < 4; ++e) {
@@ -320,7 +329,7 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(KvView c, KvAttnArgs a, 
       if (y[0] != x[0] || y[1] != x[1] || y[2] != x[2] || y[3] != x[3]) {
         *at_v = y;
         const int k = 16 * wave + kRows * i + lrow;
-        if (t0 + k < tl.n) atomicOr(&odd[s & 3][k >> 5], 1u << (k & 31));
+        if (t0 + k < tl.n && (lpos ^ R::fv(lrow)) < chunks) atomicOr(&odd[s & 3][k >> 5], 1u << (k & 31));
       }
     }
   };
@@ -342,14 +351,28 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(KvView c, KvAttnArgs a, 
     for (int i = 0; i < NO; ++i)
       at_v[i] = R::kHalf + r * R::kPitch + (((4 * i + 2 * ((lane >> 4) & 1) + ((j & 3) >> 1)) ^ R::fv(r)) * 16) + 8 * (j & 1);
   }
-  // scores of the 32 slots u of a tile
-  auto scores = [&](const GPTQ_LDS char* b, int u) __attribute__((always_inline)) {
+  // Operands are read from LDS well before the products that take them: a read takes longer
+  // than a product, and left to itself the compiler waits for each in turn.
+  struct Keys {
+    x8 f[QS];
+  };
+  struct Values {
+    x8 f[2][NO];
+  };
+  auto keys = [&](const GPTQ_LDS char* b, int u) __attribute__((always_inline)) {
+    Keys k;
+#pragma unroll
+    for (int i = 0; i < QS; ++i) k.f[i] = *(const GPTQ_LDS x8*)(b + at_k[i] + 32 * u * R::kPitch);
+    return k;
+  };
+  auto scores = [&](const Keys& k) __attribute__((always_inline)) {
     float16v x = (float16v){0};
 #pragma unroll
-    for (int i = 0; i < QS; ++i) x = KT::mfma32(*(const GPTQ_LDS x8*)(b + at_k[i] + 32 * u * R::kPitch), q[i], x);
+    for (int i = 0; i < QS; ++i) x = KT::mfma32(k.f[i], q[i], x);
     return x;
   };
   auto mask = [&](float16v& x, int t0, uint32_t page_bits) __attribute__((always_inline)) {
+    asm volatile("" : "+v"(t0));  // (or its arithmetic is taken out in front of the branch to here)
     const uint32_t see = (seen(t0) & page_bits) >> (8 * half);
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
@@ -368,20 +391,30 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(KvView c, KvAttnArgs a, 
       pf[r >> 3][r & 7] = (T)p;
     }
   };
-  auto values = [&](const GPTQ_LDS char* b, int u, const x8(&pf)[2]) __attribute__((always_inline)) {
+  auto values = [&](const GPTQ_LDS char* b, int u) __attribute__((always_inline)) {
+    Values v;
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
       for (int i = 0; i < NO; ++i) {
         const GPTQ_LDS char* p = b + at_v[i] + (32 * u + 16 * k) * R::kPitch;
         const short4v lo = lds_tr(p), hi = lds_tr(p + 4 * R::kPitch);
-        o[i] = KT::mfma32(__builtin_bit_cast(x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7)), pf[k], o[i]);
+        v.f[k][i] = __builtin_bit_cast(x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
       }
+    return v;
+  };
+  auto weigh = [&](const Values& v, const x8(&pf)[2]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int i = 0; i < NO; ++i) o[i] = KT::mfma32(v.f[k][i], pf[k], o[i]);
   };
   // rare: values of a tile that are not finite, for the queries that see them (their weight is
   // positive, so the sum is what the value is)
   auto add_odd = [&](int t0, uint32_t bits) __attribute__((always_inline)) {
-    const uint32_t see = seen(t0);
+    int at0 = t0;
+    asm volatile("" : "+v"(at0));
+    const uint32_t see = seen(at0);
     for (int k = 0; k < 32; ++k) {
       if (!((bits >> k) & 1)) continue;
       const int t = t0 + k, pg = table[t >> c.page_shift];
@@ -409,30 +442,11 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(KvView c, KvAttnArgs a, 
     int pg = pages(0), pg_next = pages(1);
     __syncthreads();
     stage(0, pg);
-    for (int s = 0; s < tl.total; ++s) {
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");  // this wave's rows of tile s have landed
-      const bool in_part = s < all_lo || s >= all_hi;
-      if (in_part) clean(s);
-      if (tid < 2) odd[(s + 2) & 3][tid] = 0u;  // read last by tile s - 2, written next two barriers from here
-      lds_barrier();  // tile s is in LDS for every wave, tile s - 1 is read by none
-      const uint64_t good = __ballot(c.page_ok(pg));
-      const uint32_t on_page = (uint32_t)(good >> (8 * (s & 7))) & 0xffu;
-      if ((s & 7) == 7) {
-        pg = pg_next;
-        pg_next = pages((s >> 3) + 2);
-      }
-      if (s + 1 < tl.total) stage(s + 1, pg);
-      if (hidden(s)) continue;
-      const GPTQ_LDS char* b = lds + (s & 1) * R::kTileBytes;
-      const int t0 = tl.slot0(s);
-      float16v x = scores(b, 0), y = scores(b, 1);
-      if (s < full_lo || s >= full_hi || on_page != 0xffu) {
-        mask(x, t0, octet_bits(on_page));
-        mask(y, t0 + 32, octet_bits(on_page >> 4));
-      }
+    // raises the running maximum to those of x and y if a score is far above it
+    auto raise_to = [&](const float16v& x, const float16v& y) __attribute__((always_inline)) {
       float top = fmaxf(x[0], y[0]);
 #pragma unroll
-      for (int r = 1; r < 16; ++r) top = fmaxf(top, fmaxf(x[r], y[r]));
+      for (int r = 1; r < 16; ++r) top = fmaxf(fmaxf(top, x[r]), y[r]);
       if (__any(top > m + raise)) {
         const float nm = fmaxf(m, fmaxf(top, __shfl_xor(top, 32)));
         const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m - nm) * sc);
@@ -441,13 +455,49 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(KvView c, KvAttnArgs a, 
 #pragma unroll
         for (int i = 0; i < NO; ++i) o[i] *= f;
       }
-      const float base = m == -INFINITY ? 0.0f : m * sc;
-      x8 px[2], py[2];
-      softmax(x, base, px);
-      values(b, 0, px);
-      softmax(y, base, py);
-      values(b, 1, py);
+      return m == -INFINITY ? 0.0f : m * sc;
+    };
+    for (int s = 0; s < tl.total; ++s) {
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");  // this wave's rows of tile s have landed
+      const bool in_part = s < all_lo || s >= all_hi;
       if (in_part) {
+        clean(s);
+        if (tid < 2) odd[(s + 2) & 3][tid] = 0u;  // read last by tile s - 2, written next two barriers from here
+      }
+      lds_barrier();  // tile s is in LDS for every wave, tile s - 1 is read by none
+      const uint64_t good = __ballot(c.page_ok(pg));
+      const uint32_t on_page = (uint32_t)(good >> (8 * (s & 7))) & 0xffu;
+      if ((s & 7) == 7) {
+        pg = pg_next;
+        pg_next = pages((s >> 3) + 2);
+      }
+      if (s + 1 < tl.total) stage(s + 1, pg);
+      const GPTQ_LDS char* b = lds + (s & 1) * R::kTileBytes;
+      x8 px[2], py[2];
+      if (!in_part && on_page == 0xffu) {
+        // every query sees all of it: one straight piece of code
+        const Keys k0 = keys(b, 0), k1 = keys(b, 1);
+        __builtin_amdgcn_sched_barrier(0);
+        float16v x = scores(k0), y = scores(k1);
+        const float base = raise_to(x, y);
+        const Values v0 = values(b, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        softmax(x, base, px);
+        __builtin_amdgcn_sched_barrier(0);
+        const Values v1 = values(b, 1);
+        weigh(v0, px);
+        softmax(y, base, py);
+        weigh(v1, py);
+      } else if (!hidden(s)) {
+        const int t0 = tl.slot0(s);
+        float16v x = scores(keys(b, 0)), y = scores(keys(b, 1));
+        mask(x, t0, octet_bits(on_page));
+        mask(y, t0 + 32, octet_bits(on_page >> 4));
+        const float base = raise_to(x, y);
+        softmax(x, base, px);
+        weigh(values(b, 0), px);
+        softmax(y, base, py);
+        weigh(values(b, 1), py);
         const uint32_t o0 = uni((int)odd[s & 3][0]), o1 = uni((int)odd[s & 3][1]);
         if (o0) add_odd(t0, o0);
         if (o1) add_odd(t0 + 32, o1);
@@ -484,29 +534,34 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(KvView c, KvAttnArgs a, 
 // 2^(score - lse): the scores once more (half the products of the attention),
 // as S^T tiles whose rows, the slots, are summed along. One block owns 128 slots
 // of one key head (a wave 32, its keys in registers) and goes over all queries
-// that may see them, 32 at a time, so every sum has one owner and one order.
-template <typename T, int DHP>
+// that may see them, 64 at a time through LDS (DMA, the next 64 while these are
+// used), so every sum has one owner and one order. Bound by the exponentials:
+// 16 per lane for 32 x 32 scores take 256 cycles, the products 32 QS.
+template <typename T, int QS>
 __global__ __launch_bounds__(256, 2) void prompt_weights_kernel(KvView c, KvAttnArgs a, const int32_t* cu, int n_rows,
-                                                               int n_tiles, const float* lse) {
+                                                               const float* lse) {
   using KT = KvType<T>;
   using x8 = typename KT::x8;
-  constexpr int QS = DHP / 16, CH = DHP / 8, QP = DHP + 8, NQ = 64;
-  __shared__ __attribute__((aligned(16))) T qs[NQ * QP];
-  __shared__ float ls[NQ];
-  const int id = xcd_logical_block(blockIdx.x, gridDim.x);
-  const int tile = id % n_tiles, bg = id / n_tiles;
+  using R = Ring<QS>;
+  constexpr int kRows = 64 / R::kLpr, kDma = 16 / kRows, kBytes = kT * R::kPitch;
+  __shared__ __attribute__((aligned(1024))) char smem[2 * kBytes];
+  const GPTQ_LDS char* lds = (const GPTQ_LDS char*)smem;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
+  // the first slots, which most queries see, of all sequences and heads first
+  const int tile = blockIdx.x / (c.n_kv * c.n_seqs), bg = blockIdx.x - tile * (c.n_kv * c.n_seqs);
   const int kvh = bg % c.n_kv, b = bg / c.n_kv;
-  const int r0 = cu[b], r1 = cu[b + 1];
-  const int len = c.len(b);
+  const int r0 = uni(cu[b]), r1 = uni(cu[b + 1]);
+  const int len = uni(c.len(b));
   const int n_b = r0 >= 0 && r1 > r0 && r1 <= n_rows ? r1 - r0 : 0;
   const int t00 = tile * 128;
   if (n_b == 0 || t00 >= len) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
   const int col = lane & 31, half = lane >> 5;
   const int t0 = t00 + 32 * wave;
   const int group = a.n_heads / c.n_kv, chunks = c.dim >> 3;
   const int32_t* table = c.table + (int64_t)b * c.ld_table;
-  const float sc = a.scale * kLog2e;
+  const float sc = fmaxf(__builtin_fabsf(a.scale) * kLog2e, 1e-30f);
+  const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
 
   x8 k[QS];
   {
@@ -517,7 +572,7 @@ __global__ __launch_bounds__(256, 2) void prompt_weights_kernel(KvView c, KvAttn
     for (int i = 0; i < QS; ++i) {
       const int ch = 2 * i + half;
       const bool ok = ch < chunks && c.page_ok(pg);
-      const uint4v z = *(const uint4v*)(kp + 8 * (ok ? ch : 0));
+      const uint4v z = *(const uint4v*)(kp + 8 * (ok ? ch : 0)) ^ (uint4v){flip, flip, flip, flip};
       k[i] = __builtin_bit_cast(x8, (uint4v){ok ? z[0] : 0u, ok ? z[1] : 0u, ok ? z[2] : 0u, ok ? z[3] : 0u});
     }
   }
@@ -530,37 +585,83 @@ __global__ __launch_bounds__(256, 2) void prompt_weights_kernel(KvView c, KvAttn
     const int64_t last = (int64_t)t00 + 127 + a.window - base;  // first query that no longer sees slot t00 + 127
     if (last < i_hi) i_hi = (int)last;
   }
-  i_lo &= ~(NQ - 1);
-  const T* qb = (const T*)a.q + (int64_t)r0 * a.ldq;
-  for (int hh = 0; hh < group; ++hh) {
-    const int h = kvh * group + hh;
-    for (int i0 = i_lo; i0 < i_hi; i0 += NQ) {
-      __syncthreads();
-      for (int it = tid; it < NQ * CH; it += 256) {
-        const int row = it / CH, ch = it - row * CH;
-        uint4v z = (uint4v){0, 0, 0, 0};
-        if (i0 + row < n_b && ch < chunks) z = *(const uint4v*)(qb + (int64_t)(i0 + row) * a.ldq + (int64_t)h * c.dim + ch * 8);
-        *(uint4v*)&qs[row * QP + ch * 8] = z;
-      }
-      if (tid < NQ) ls[tid] = i0 + tid < n_b ? lse[(int64_t)(r0 + i0 + tid) * a.n_heads + h] : INFINITY;
-      __syncthreads();
+  i_lo &= ~(kT - 1);
+  const int steps = i_hi > i_lo ? (i_hi - i_lo + kT - 1) / kT : 0, total = steps * group;
+
+  // this wave's 16 rows of every 64 queries; rows behind the last repeat it (and are masked)
+  const int lrow = lane / R::kLpr, lpos = lane % R::kLpr;
+  const bool exact = c.dim == 16 * QS;
+  const T* qb = (const T*)a.q + (int64_t)r0 * a.ldq + (int64_t)kvh * group * c.dim;
+  // 64 queries of one head: the head and the first query
+  struct At {
+    int hh, i;
+  };
+  auto after = [&](At p) __attribute__((always_inline)) {
+    return p.i + kT < i_hi ? At{p.hh, p.i + kT} : At{p.hh + 1, i_lo};
+  };
+  auto stage = [&](int s, At p) __attribute__((always_inline)) {
+    const int hh = p.hh, i0 = p.i + 16 * wave;
+    const uint32_t to = lds0 + (s & 1) * kBytes + 16 * wave * R::kPitch;
+    const T* from = qb + uni((int64_t)(i0 < n_b ? i0 : n_b - 1) * a.ldq + (int64_t)hh * c.dim);
+    const int left = i0 < n_b ? n_b - 1 - i0 : 0;  // last row that is there
 #pragma unroll
-      for (int u = 0; u < NQ / 32; ++u) {
-        float16v sv = (float16v){0};
+    for (int i = 0; i < kDma; ++i) {
+      const int r = kRows * i + lrow, ch = lpos ^ R::fk(r);
+      const uint32_t off = (uint32_t)((r < left ? r : left) * (uint32_t)a.ldq + (ch < chunks ? ch : 0) * 8) * 2;
+      if (exact || ch < chunks) dma16_from(from, off, to + 1024 * i);
+    }
+  };
+  auto row_lse = [&](At p, int u) __attribute__((always_inline)) {
+    const int i = p.i + 32 * u + col;
+    return lse[(int64_t)(r0 + (i < n_b ? i : n_b - 1)) * a.n_heads + kvh * group + p.hh];
+  };
+  const int qrow = col;
+  uint32_t at_q[QS];
 #pragma unroll
-        for (int i = 0; i < QS; ++i) sv = KT::mfma32(k[i], *(const x8*)&qs[(32 * u + col) * QP + 16 * i + 8 * half], sv);
-        const int pos = base + i0 + 32 * u + col;
-        const float l = ls[32 * u + col];
+  for (int i = 0; i < QS; ++i) at_q[i] = qrow * R::kPitch + (((2 * i + half) ^ R::fk(qrow)) * 16);
+
+  if (total > 0) {
+    if (!exact)
+      for (int i = tid; i < 2 * kBytes / 16; i += 256) *(GPTQ_LDS uint4v*)(lds + 16 * i) = (uint4v){0, 0, 0, 0};
+    __syncthreads();
+    At now = {0, i_lo};
+    stage(0, now);
+    float l0 = row_lse(now, 0), l1 = row_lse(now, 1);
+    for (int s = 0; s < total; ++s) {
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      lds_barrier();
+      const At next = s + 1 < total ? after(now) : now;
+      if (s + 1 < total) stage(s + 1, next);
+      const float n0 = row_lse(next, 0), n1 = row_lse(next, 1);
+      const GPTQ_LDS char* buf = lds + (s & 1) * kBytes;
+      const int i0 = now.i;
+      now = next;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        float16v x = (float16v){0};
+#pragma unroll
+        for (int i = 0; i < QS; ++i) x = KT::mfma32(k[i], *(const GPTQ_LDS x8*)(buf + at_q[i] + 32 * u * R::kPitch), x);
+        const float l = u ? l1 : l0;
         const int lowest = base + i0 + 32 * u;
-        const bool all = t0 + 31 <= lowest && (a.window <= 0 || t0 > lowest + 31 - a.window || t0 + 32 <= a.sinks);
+        if (t0 + 31 <= lowest && i0 + 32 * u + 32 <= n_b &&
+            (a.window <= 0 || t0 > lowest + 31 - a.window || t0 + 32 <= a.sinks)) {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int t = t0 + 16 * (r >> 3) + 8 * half + (r & 7);
-          const bool ok = all || (t <= pos && (a.window <= 0 || t > pos - a.window || t < a.sinks));
-          const float p = __builtin_amdgcn_exp2f(sv[r] * sc - l);
-          acc[r] += ok ? p : 0.0f;
+          for (int r = 0; r < 16; ++r) acc[r] += __builtin_amdgcn_exp2f(fmaf(x[r], sc, -l));
+        } else {
+          const int pos = lowest + col;
+          uint32_t see = low_bits(pos + 1 - t0);
+          if (a.window > 0) see &= ~low_bits(pos + 1 - a.window - t0) | low_bits(a.sinks - t0);
+          if (i0 + 32 * u + col >= n_b) see = 0;
+          see >>= 8 * half;
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const float p = __builtin_amdgcn_exp2f(fmaf(x[r], sc, -l));
+            acc[r] += (see >> (16 * (r >> 3) + (r & 7))) & 1 ? p : 0.0f;
+          }
         }
       }
+      l0 = n0;
+      l1 = n1;
     }
   }
 #pragma unroll
@@ -597,8 +698,8 @@ gptq_status_t launch(const KvView& c, const KvAttnArgs& a, const int32_t* cu, in
   const gptq_status_t rc = a.weights ? launch_rows<T, QS, true>(c, a, cu, n_tokens, lse, st)
                                      : launch_rows<T, QS, false>(c, a, cu, n_tokens, lse, st);
   if (rc != GPTQ_OK || !a.weights) return rc;
-  hipLaunchKernelGGL((prompt_weights_kernel<T, 16 * QS>), dim3((unsigned)wblocks), dim3(256), 0, st, c, a, cu,
-                     (int)n_tokens, (int)n_tiles, lse);
+  hipLaunchKernelGGL((prompt_weights_kernel<T, QS>), dim3((unsigned)wblocks), dim3(256), 0, st, c, a, cu,
+                     (int)n_tokens, lse);
   GPTQ_CHECK_LAUNCH();
   return GPTQ_OK;
 }
