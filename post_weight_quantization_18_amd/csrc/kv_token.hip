@@ -26,6 +26,8 @@
 // The slots are split over the waves of a block and over n_splits blocks; a
 // block's waves are joined through LDS, the blocks by a second kernel (which also
 // turns the stored scores into weights).
+#include <algorithm>
+
 #include "kv.h"
 
 namespace gptq {
@@ -60,7 +62,41 @@ struct TokenWs {
   float* o;       // [n_seqs * n_heads][n_splits][dim]
   float* scores;  // [n_seqs * n_heads][n_scores]
   int n_splits, n_scores;
+  bool join;  // a second kernel
 };
+
+// weights += 2^(score - m) / l, summed over the heads of a group, for the steps [s0,
+// s1) of one sequence and key head; sh holds m and 1 / l of each head. 256 threads, four
+// slots each at a time.
+__device__ __forceinline__ void add_weights(const KvView& c, const KvAttnArgs& a, const TokenWs& w, const Steps& st,
+                                            int b, int kvh, int s0, int s1, const float* sh) {
+  const int group = a.n_heads / c.n_kv;
+  const float* sp = w.scores + ((int64_t)b * a.n_heads + kvh * group) * w.n_scores;
+  float* wt = a.weights + ((int64_t)b * c.n_kv + kvh) * a.ldw;
+  const int end = (s1 < st.total ? s1 : st.total) * kTile;
+  for (int k0 = s0 * kTile + threadIdx.x; k0 < end; k0 += 1024) {
+    float add[4] = {0, 0, 0, 0}, old[4];
+    int t[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = k0 + 256 * i;
+      t[i] = -1;
+      if (k < end) {
+        const int slot = st.slot0(k / kTile) + k % kTile;
+        if (slot < st.n && (slot >= st.first || slot < a.sinks)) t[i] = slot;
+      }
+      old[i] = t[i] >= 0 ? wt[t[i]] : 0.0f;
+    }
+    for (int h = 0; h < group; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (t[i] >= 0)
+          add[i] += __builtin_amdgcn_exp2f(sp[(int64_t)h * w.n_scores + k0 + 256 * i] - sh[2 * h]) * sh[2 * h + 1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (t[i] >= 0) wt[t[i]] = old[i] + add[i];
+  }
+}
 
 template <typename T, int KS, int VEC>
 struct TokenRegs {
@@ -69,7 +105,7 @@ struct TokenRegs {
 };
 
 // KS: steps of 32 along the head for the scores; VEC: output elements per lane
-// (16 VEC >= dim). SPLIT: partial results to the workspace. SCORES: they are
+// (16 VEC >= dim). SPLIT: partial results to the workspace. SCORES: the
 // stored too.
 template <typename T, int KS, int VEC, bool SPLIT, bool SCORES>
 __global__ __launch_bounds__(64 * kWaves, 2) void token_kernel(KvView c, KvAttnArgs a, TokenWs w) {
@@ -261,7 +297,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void token_kernel(KvView c, KvAttnA
   // join the waves of the block
   lsum += __shfl_xor(lsum, 16);
   lsum += __shfl_xor(lsum, 32);
-  __shared__ float sm[kWaves][16], sl[kWaves][16];
+  __shared__ float sm[kWaves][16], sl[kWaves][16], fin[32];
   __shared__ float so[kWaves][16][16 * VEC + 4];
   if (g == 0) {
     sm[wave][cl] = m;
@@ -296,61 +332,85 @@ __global__ __launch_bounds__(64 * kWaves, 2) void token_kernel(KvView c, KvAttnA
       }
     } else {
       ((T*)a.out)[(int64_t)b * a.ldo + (int64_t)(kvh * group + h0 + hh) * c.dim + e] = (T)(l == 0.0f ? 0.0f : v / l);
+      if (SCORES && e == 0) {
+        fin[2 * hh] = mm == -INFINITY ? 0.0f : mm;
+        fin[2 * hh + 1] = l == 0.0f ? 0.0f : 1.0f / l;
+      }
     }
+  }
+  if constexpr (SCORES && !SPLIT) {
+    // this block has seen all scores of its key head: its own writes, read back
+    __syncthreads();
+    add_weights(c, a, w, st, b, kvh, 0, st.total, fin);
   }
 }
 
-// Joins the splits of one (sequence, key head): block part 0 the outputs of its
-// heads, every part the weights of its steps. Each head's maximum and sum over
-// the splits are found again by every block (a few hundred bytes).
-constexpr int kJoinSteps = 32;  // steps whose weights one block adds
+// Maximum and sum of one head over its splits, by a wave (every lane returns them).
+__device__ __forceinline__ void join_ml(const float* ml, int n_splits, float* m, float* l) {
+  const int lane = threadIdx.x & 63;
+  float mm = -INFINITY, ll = 0.0f;
+  for (int s = lane; s < n_splits; s += 64) mm = fmaxf(mm, ml[2 * s]);
+  for (int o = 32; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor(mm, o));
+  const float base = mm == -INFINITY ? 0.0f : mm;  // (a sum over nothing visible is 0 or, from a NaN score, NaN)
+  for (int s = lane; s < n_splits; s += 64) ll += __builtin_amdgcn_exp2f(ml[2 * s] - base) * ml[2 * s + 1] + 0.0f * ml[2 * s + 1];
+  for (int o = 32; o > 0; o >>= 1) ll += __shfl_xor(ll, o);
+  *m = base;
+  *l = ll;
+}
+
+// Joins the splits: the first n_seqs n_heads blocks one head's output each (8
+// groups of threads take every eighth split, 4 elements a thread), the others the
+// weights of kJoinSteps steps of one key head.
+constexpr int kJoinSteps = 32;
 
 template <typename T>
 __global__ __launch_bounds__(256) void token_join_kernel(KvView c, KvAttnArgs a, TokenWs w, int n_parts) {
-  extern __shared__ float sh[];  // per head of the group: maximum, 1 / sum
+  extern __shared__ float sh[];
+  const int tid = threadIdx.x;
+  if ((int)blockIdx.x < c.n_seqs * a.n_heads) {
+    const int64_t bh = blockIdx.x;
+    const float* ml = w.ml + bh * w.n_splits * 2;
+    float m, l;
+    join_ml(ml, w.n_splits, &m, &l);
+    const int g = tid >> 5, e = (tid & 31) * 4;
+    const bool in = e < c.dim;
+    const float* o = w.o + bh * w.n_splits * c.dim + (in ? e : 0);
+    float4v v = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int s = g; s < w.n_splits; s += 8)
+      v += __builtin_amdgcn_exp2f(ml[2 * s] - m) * *(const float4v*)(o + (int64_t)s * c.dim);
+    *(float4v*)(sh + 4 * tid) = v;
+    __syncthreads();
+    if (g == 0 && in) {
+#pragma unroll
+      for (int k = 1; k < 8; ++k) v += *(const float4v*)(sh + 4 * (tid + 32 * k));
+      const int b = bh / a.n_heads, h = bh - (int64_t)b * a.n_heads;
+      typedef T x4 __attribute__((ext_vector_type(4)));
+      x4 y;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) y[k] = (T)(l == 0.0f ? 0.0f : v[k] / l);
+      *(x4*)((T*)a.out + (int64_t)b * a.ldo + (int64_t)h * c.dim + e) = y;
+    }
+    return;
+  }
   const int group = a.n_heads / c.n_kv;
-  int id = blockIdx.x;
+  int id = blockIdx.x - c.n_seqs * a.n_heads;
   const int part = id % n_parts;
   id /= n_parts;
   const int kvh = id % c.n_kv, b = id / c.n_kv;
+  const Steps st(c.len(b), a.window, a.sinks);
+  if (part * kJoinSteps >= st.total) return;
   const int64_t bh0 = (int64_t)b * a.n_heads + kvh * group;
-  for (int h = threadIdx.x >> 6; h < group; h += 4) {
-    const float* ml = w.ml + (bh0 + h) * w.n_splits * 2;
-    float mm = -INFINITY, l = 0.0f;
-    for (int s = threadIdx.x & 63; s < w.n_splits; s += 64) mm = fmaxf(mm, ml[2 * s]);
-    for (int o = 32; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor(mm, o));
-    for (int s = threadIdx.x & 63; s < w.n_splits; s += 64)
-      l += ml[2 * s] == -INFINITY ? ml[2 * s + 1] : exp2f(ml[2 * s] - mm) * ml[2 * s + 1];
-    for (int o = 32; o > 0; o >>= 1) l += __shfl_xor(l, o);
-    if ((threadIdx.x & 63) == 0) {
-      sh[2 * h] = mm == -INFINITY ? 0.0f : mm;
+  for (int h = tid >> 6; h < group; h += 4) {
+    float m, l;
+    join_ml(w.ml + (bh0 + h) * w.n_splits * 2, w.n_splits, &m, &l);
+    if ((tid & 63) == 0) {
+      sh[2 * h] = m;
       sh[2 * h + 1] = l == 0.0f ? 0.0f : 1.0f / l;
     }
   }
   __syncthreads();
-  if (part == 0) {
-    for (int k = threadIdx.x; k < group * c.dim; k += 256) {
-      const int h = k / c.dim, e = k - h * c.dim;
-      const float* ml = w.ml + (bh0 + h) * w.n_splits * 2;
-      const float* o = w.o + (bh0 + h) * w.n_splits * c.dim + e;
-      float v = 0.0f;
-      for (int s = 0; s < w.n_splits; ++s)
-        v += ml[2 * s] == -INFINITY ? o[(int64_t)s * c.dim] : exp2f(ml[2 * s] - sh[2 * h]) * o[(int64_t)s * c.dim];
-      ((T*)a.out)[(int64_t)b * a.ldo + (int64_t)(kvh * group + h) * c.dim + e] = (T)(v * sh[2 * h + 1]);
-    }
-  }
-  if (!a.weights) return;
-  const Steps st(c.len(b), a.window, a.sinks);
-  const int s1 = (part + 1) * kJoinSteps < st.total ? (part + 1) * kJoinSteps : st.total;
-  float* wt = a.weights + ((int64_t)b * c.n_kv + kvh) * a.ldw;
-  for (int k = part * kJoinSteps * kTile + threadIdx.x; k < s1 * kTile; k += 256) {
-    const int t = st.slot0(k / kTile) + k % kTile;
-    if (t >= st.n || (t < st.first && t >= a.sinks)) continue;
-    float add = 0.0f;
-    for (int h = 0; h < group; ++h)
-      add += exp2f(w.scores[(bh0 + h) * w.n_scores + k] - sh[2 * h]) * sh[2 * h + 1];
-    wt[t] += add;
-  }
+  add_weights(c, a, w, st, b, kvh, part * kJoinSteps, (part + 1) * kJoinSteps, sh);
 }
 
 int64_t max_steps(const KvView& c, int64_t window, int64_t sinks) {
@@ -373,13 +433,14 @@ int64_t splits_of(const KvView& c, int64_t n_heads, int64_t window, int64_t sink
 TokenWs layout(const KvView& c, int64_t n_heads, int64_t window, int64_t sinks, bool weights, void* ws, size_t* bytes) {
   TokenWs w{};
   w.n_splits = (int)splits_of(c, n_heads, window, sinks);
+  w.join = w.n_splits > 1 || (weights && n_heads / c.n_kv > 16);
   w.n_scores = (int)(max_steps(c, window, sinks) * kTile);
   const int64_t rows = (int64_t)c.n_seqs * n_heads;
   float* p = (float*)ws;
   size_t n = 0;
-  if (w.n_splits > 1 || weights) {
-    w.scores = p + n;  // first: 16-byte aligned
-    if (weights) n += (size_t)rows * w.n_scores;
+  w.scores = p;  // multiples of 4 floats each: all 16-byte aligned
+  if (weights) n += (size_t)rows * w.n_scores;
+  if (w.join) {
     w.o = p + n;
     n += (size_t)rows * w.n_splits * c.dim;
     w.ml = p + n;
@@ -394,9 +455,11 @@ gptq_status_t launch(const KvView& c, const KvAttnArgs& a, const TokenWs& w, hip
   const int64_t blocks = (int64_t)c.n_seqs * c.n_kv * ceil_div(a.n_heads / c.n_kv, 16) * w.n_splits;
   if (blocks * 64 * kWaves >= (int64_t)1 << 32) return GPTQ_ERR_UNSUPPORTED;
   const dim3 grid((unsigned)blocks), blk(64 * kWaves);
-  if (a.weights)
+  if (a.weights && w.join)
     hipLaunchKernelGGL((token_kernel<T, KS, VEC, true, true>), grid, blk, 0, st, c, a, w);
-  else if (w.n_splits > 1)
+  else if (a.weights)
+    hipLaunchKernelGGL((token_kernel<T, KS, VEC, false, true>), grid, blk, 0, st, c, a, w);
+  else if (w.join)
     hipLaunchKernelGGL((token_kernel<T, KS, VEC, true, false>), grid, blk, 0, st, c, a, w);
   else
     hipLaunchKernelGGL((token_kernel<T, KS, VEC, false, false>), grid, blk, 0, st, c, a, w);
@@ -408,7 +471,7 @@ template <typename T>
 gptq_status_t token_enqueue(const KvView& c, const KvAttnArgs& a, void* ws, hipStream_t st) {
   const TokenWs w = layout(c, a.n_heads, a.window, a.sinks, a.weights != nullptr, ws, nullptr);
   const int64_t parts = a.weights ? ceil_div(w.n_scores / kTile, kJoinSteps) : 1;
-  const int64_t jblocks = (int64_t)c.n_seqs * c.n_kv * parts;
+  const int64_t jblocks = (int64_t)c.n_seqs * (a.n_heads + (a.weights ? c.n_kv * parts : 0));
   if (jblocks * 256 >= (int64_t)1 << 32) return GPTQ_ERR_UNSUPPORTED;
   gptq_status_t rc;
   if (c.dim <= 64)
@@ -417,9 +480,9 @@ gptq_status_t token_enqueue(const KvView& c, const KvAttnArgs& a, void* ws, hipS
     rc = launch<T, 3, 8>(c, a, w, st);
   else
     rc = launch<T, 4, 8>(c, a, w, st);
-  if (rc != GPTQ_OK || (w.n_splits == 1 && !a.weights)) return rc;
+  if (rc != GPTQ_OK || !w.join) return rc;
   hipLaunchKernelGGL(token_join_kernel<T>, dim3((unsigned)jblocks), dim3(256),
-                     2 * sizeof(float) * (a.n_heads / c.n_kv), st, c, a, w, (int)parts);
+                     std::max<size_t>(4096, 2 * sizeof(float) * (a.n_heads / c.n_kv)), st, c, a, w, (int)parts);
   GPTQ_CHECK_LAUNCH();
   return GPTQ_OK;
 }

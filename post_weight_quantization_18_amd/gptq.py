@@ -417,45 +417,53 @@ def pack_codes(codes: torch.Tensor, bits: int) -> torch.Tensor:
 _KV_DT = {torch.float16: GPTQ_F16, torch.bfloat16: GPTQ_BF16}
 
 
-def _kv(k, v, page_table, lens, *others):
-    """The cache and its sequences as the library takes them, checked: dtypes,
-    shapes and one device for these and every tensor of `others` (or None)."""
+def _kv(k, v, page_table, lens):
+    """The cache and its sequences as the library takes them, dtypes and shapes checked."""
     _need_cuda(k, "k")
-    dev = k.device
-    for t in (v, page_table, lens, *others):
-        if t is not None and t.device != dev:
-            raise ValueError("every tensor must be on the cache's device")
-    if k.dtype not in _KV_DT or v.dtype != k.dtype:
+    dt = _KV_DT.get(k.dtype)
+    if dt is None or v.dtype != k.dtype:
         raise ValueError("k and v must be fp16 or bf16, both the same")
-    if k.dim() != 4 or v.shape != k.shape:
+    shape, strides = k.shape, k.stride()
+    if len(shape) != 4 or v.shape != shape:
         raise ValueError("k and v must be [n_pages, n_kv_heads, page_size, head_dim]")
-    n_pages, n_kv, ps, dim = k.shape
-    if k.stride() != v.stride() or k.stride()[1:] != (ps * dim, dim, 1):
+    n_pages, n_kv, ps, dim = shape
+    if v.stride() != strides or strides[3] != 1 or strides[2] != dim or strides[1] != ps * dim:
         raise ValueError("k and v: equal strides, contiguous within a page")
     if page_table.dtype != torch.int32 or lens.dtype != torch.int32:
         raise ValueError("page_table and lens must be int32")
-    if page_table.dim() != 2 or lens.dim() != 1 or page_table.shape[0] != lens.shape[0]:
+    if page_table.dim() != 2 or lens.dim() != 1:
         raise ValueError("page_table [n_seqs, max_pages], lens [n_seqs]")
-    if page_table.stride(1) != 1 or (lens.stride(0) != 1 and lens.shape[0] > 1):
-        raise ValueError("page_table rows and lens must be contiguous")
     n_seqs, max_pages = page_table.shape
-    cache = KvCache(k.data_ptr(), v.data_ptr(), _KV_DT[k.dtype], ps, n_kv, dim, n_pages,
-                    k.stride(0) if n_pages > 1 else n_kv * ps * dim)
-    # one row: its stride says nothing
-    seqs = KvSeqs(page_table.data_ptr(), page_table.stride(0) if n_seqs > 1 else max_pages, max_pages,
-                  lens.data_ptr(), n_seqs)
-    return cache, seqs
+    ld, one = page_table.stride()
+    if lens.shape[0] != n_seqs:
+        raise ValueError("page_table [n_seqs, max_pages], lens [n_seqs]")
+    if (one != 1 and max_pages > 1) or (n_seqs > 1 and lens.stride(0) != 1):
+        raise ValueError("page_table rows and lens must be contiguous")
+    # the stride of a single page or row says nothing
+    return (KvCache(k.data_ptr(), v.data_ptr(), dt, ps, n_kv, dim, n_pages,
+                    strides[0] if n_pages > 1 else n_kv * ps * dim),
+            KvSeqs(page_table.data_ptr(), ld if n_seqs > 1 else max_pages, max_pages, lens.data_ptr(), n_seqs))
+
+
+def _one_device(k, *others):
+    dev = k.get_device()
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("every tensor must be on the cache's device")
+    return dev
 
 
 def _rows(t, name, dtype, heads, dim):
     """Row stride of new tokens' rows [n, heads, dim], contiguous within a row."""
     if t.dtype != dtype:
         raise ValueError(f"{name} must have the cache's dtype")
-    if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != dim or (heads is not None and shape[1] != heads):
         raise ValueError(f"{name} must be [n, heads, head_dim] of the cache's head_dim")
-    if t.stride(2) != 1 or (t.stride(1) != dim and t.shape[1] > 1):
+    s = t.stride()
+    if s[2] != 1 or (s[1] != dim and shape[1] > 1):
         raise ValueError(f"{name} rows must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * dim
+    return s[0] if shape[0] > 1 else shape[1] * dim
 
 
 def _cu(cu, n_seqs):
@@ -473,6 +481,17 @@ def _weights(w, name, n_seqs, n_kv, slots):
     return w.shape[2]
 
 
+def _launch(dev, fn, what, *args):
+    """fn(*args, stream) on device dev and its current stream."""
+    if torch.cuda.current_device() == dev:
+        status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if status:
+        raise GPTQError(status, what)
+
+
 def kv_append(k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor, k_new: torch.Tensor,
               v_new: torch.Tensor, cu_seqlens: torch.Tensor | None = None):
     """New tokens' keys and values into the pages of their sequences. k, v [n_pages,
@@ -480,32 +499,16 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, lens: 
     max_pages]; lens int32 [n_seqs], the new tokens counted; k_new, v_new [n,
     n_kv_heads, head_dim], sequence b's rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1
     (int32 [n_seqs + 1]; None: one row per sequence)."""
-    lib = load_library()
-    cache, seqs = _kv(k, v, page_table, lens, k_new, v_new, cu_seqlens)
-    ldk = _rows(k_new, "k_new", k.dtype, k.shape[1], k.shape[3])
-    ldv = _rows(v_new, "v_new", k.dtype, k.shape[1], k.shape[3])
-    if k_new.shape[0] != v_new.shape[0]:
+    lib = _lib or load_library()
+    cache, seqs = _kv(k, v, page_table, lens)
+    dev = _one_device(k, v, page_table, lens, k_new, v_new, cu_seqlens)
+    ldk = _rows(k_new, "k_new", k.dtype, cache.n_kv_heads, cache.head_dim)
+    ldv = _rows(v_new, "v_new", k.dtype, cache.n_kv_heads, cache.head_dim)
+    n = k_new.shape[0]
+    if v_new.shape[0] != n:
         raise ValueError("k_new and v_new must have the same tokens")
     cu = _cu(cu_seqlens, seqs.n_seqs) if cu_seqlens is not None else None
-    with _on(k.device):
-        _check(lib.gptq_kv_append(cache, seqs, k_new.data_ptr(), ldk, v_new.data_ptr(), ldv, cu, k_new.shape[0],
-                                  torch.cuda.current_stream(k.device).cuda_stream), "gptq_kv_append")
-
-
-class _Here:
-    def __enter__(self):
-        pass
-
-    def __exit__(self, *exc):
-        pass
-
-
-_HERE_GUARD = _Here()
-
-
-def _on(device):
-    """The device of the call's tensors made current (it usually is already)."""
-    return _HERE_GUARD if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    _launch(dev, lib.gptq_kv_append, "gptq_kv_append", cache, seqs, k_new.data_ptr(), ldk, v_new.data_ptr(), ldv, cu, n)
 
 
 def kv_workspace_bytes(k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor, n_heads: int,
@@ -515,30 +518,39 @@ def kv_workspace_bytes(k: torch.Tensor, v: torch.Tensor, page_table: torch.Tenso
     return int(load_library().gptq_kv_workspace_bytes(cache, seqs, n_heads, window, sinks, n_tokens, int(weights)))
 
 
-def _attend(fn, name, q, k, v, page_table, lens, cu_seqlens, scale, window, sinks, weights, out, workspace):
-    lib = load_library()
-    cache, seqs = _kv(k, v, page_table, lens, q, cu_seqlens, weights, out, workspace)
-    dim = k.shape[3]
-    ldq = _rows(q, "q", k.dtype, None, dim)
+def _attend(fn, name, lib, q, k, v, page_table, lens, cu_seqlens, scale, window, sinks, weights, out, workspace):
+    cache, seqs = _kv(k, v, page_table, lens)
+    dev = _one_device(k, v, page_table, lens, q, cu_seqlens, weights, out, workspace)
+    dim, dtype = cache.head_dim, k.dtype
+    ldq = _rows(q, "q", dtype, None, dim)
     n, heads = q.shape[0], q.shape[1]
     if out is None:
-        out = torch.empty(n, heads, dim, dtype=q.dtype, device=q.device)
-    elif out.shape != q.shape:
-        raise ValueError("out must have the shape of q")
-    ldo = _rows(out, "out", k.dtype, heads, dim)
-    wp, ldw = None, 0
+        out = torch.empty(n, heads, dim, dtype=dtype, device=q.device)
+        ldo = heads * dim
+    else:
+        if out.shape != q.shape:
+            raise ValueError("out must have the shape of q")
+        ldo = _rows(out, "out", dtype, heads, dim)
+    wp, ldw, summed = None, 0, 0
     if weights is not None:
-        ldw = _weights(weights, "weights", seqs.n_seqs, k.shape[1], seqs.max_pages * k.shape[2])
-        wp = weights.data_ptr()
+        ldw = _weights(weights, "weights", seqs.n_seqs, cache.n_kv_heads, seqs.max_pages * cache.page_size)
+        wp, summed = weights.data_ptr(), 1
     if scale is None:
         scale = dim ** -0.5
-    rows = () if cu_seqlens is None else (_cu(cu_seqlens, seqs.n_seqs), n)
-    nbytes = lib.gptq_kv_workspace_bytes(cache, seqs, heads, window, sinks, n if rows else 0, int(weights is not None))
-    with _on(k.device):
-        ws = _workspace(nbytes, k.device, workspace)
-        _check(fn(lib)(cache, seqs, q.data_ptr(), ldq, *rows, heads, scale, window, sinks, wp, ldw, out.data_ptr(), ldo,
-                       ws.data_ptr() if ws is not None else None, nbytes,
-                       torch.cuda.current_stream(k.device).cuda_stream), name)
+    if cu_seqlens is None:
+        if n != seqs.n_seqs:
+            raise ValueError("q must have one row per sequence")
+        rows = ()
+        nbytes = lib.gptq_kv_workspace_bytes(cache, seqs, heads, window, sinks, 0, summed)
+    else:
+        rows = (_cu(cu_seqlens, seqs.n_seqs), n)
+        nbytes = lib.gptq_kv_workspace_bytes(cache, seqs, heads, window, sinks, n, summed) if summed else 0
+    ws = None
+    if nbytes:
+        workspace = _workspace(nbytes, q.device, workspace)
+        ws = workspace.data_ptr()
+    _launch(dev, fn, name, cache, seqs, q.data_ptr(), ldq, *rows, heads, scale, window, sinks, wp, ldw, out.data_ptr(),
+            ldo, ws, nbytes)
     return out
 
 
@@ -551,10 +563,9 @@ def paged_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, page_tabl
     to head_dim^-0.5. weights fp32 [n_seqs, n_kv_heads, slots] (slots >= max_pages *
     page_size): every visible slot's attention weight is added, summed over the heads
     that share its key."""
-    if q.dim() == 3 and q.shape[0] != page_table.shape[0]:
-        raise ValueError("q must have one row per sequence")
-    return _attend(lambda lib: lib.gptq_paged_attention, "gptq_paged_attention", q, k, v, page_table, lens, None, scale,
-                   window, sinks, weights, out, workspace)
+    lib = _lib or load_library()
+    return _attend(lib.gptq_paged_attention, "gptq_paged_attention", lib, q, k, v, page_table, lens, None, scale, window,
+                   sinks, weights, out, workspace)
 
 
 def paged_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,
@@ -565,8 +576,11 @@ def paged_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, page_table:
     pages: rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of q [n, n_heads, head_dim] are
     the last tokens of sequence b. Rows behind the last sequence stay as `out` held
     them. Other arguments as paged_attention."""
-    return _attend(lambda lib: lib.gptq_paged_prefill, "gptq_paged_prefill", q, k, v, page_table, lens, cu_seqlens,
-                   scale, window, sinks, weights, out, workspace)
+    lib = _lib or load_library()
+    if cu_seqlens is None:
+        raise ValueError("cu_seqlens must be int32 [n_seqs + 1]")
+    return _attend(lib.gptq_paged_prefill, "gptq_paged_prefill", lib, q, k, v, page_table, lens, cu_seqlens, scale,
+                   window, sinks, weights, out, workspace)
 
 
 def kv_evict(k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor, weights: torch.Tensor,
@@ -578,26 +592,28 @@ def kv_evict(k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, lens: t
     to go on with, the weights in the new order (0 behind the last slot), and
     int32 [n_seqs, n_kv_heads, budget] the old slot of every new one (-1 behind the
     last)."""
-    lib = load_library()
-    cache, seqs = _kv(k, v, page_table, lens, weights, new_pages)
-    n_seqs, max_pages = page_table.shape
-    n_kv, ps = k.shape[1], k.shape[2]
-    ldw = _weights(weights, "weights", n_seqs, n_kv, max_pages * ps)
+    lib = _lib or load_library()
+    cache, seqs = _kv(k, v, page_table, lens)
+    dev = _one_device(k, v, page_table, lens, weights, new_pages)
+    n_seqs, max_pages, n_kv = seqs.n_seqs, seqs.max_pages, cache.n_kv_heads
+    slots = max_pages * cache.page_size
+    ldw = _weights(weights, "weights", n_seqs, n_kv, slots)
     if new_pages.dtype != torch.int32 or new_pages.dim() != 2 or new_pages.shape[0] != n_seqs or \
             (new_pages.stride(1) != 1 and new_pages.shape[1] > 1):
         raise ValueError("new_pages must be int32 [n_seqs, pages], rows contiguous")
     if budget < 1:
         raise ValueError("budget must be positive")
-    dev = k.device
-    table_out = torch.empty(n_seqs, max_pages, dtype=torch.int32, device=dev)
-    lens_out = torch.empty(n_seqs, dtype=torch.int32, device=dev)
-    weights_out = torch.empty(n_seqs, n_kv, max_pages * ps, dtype=torch.float32, device=dev)
-    kept = torch.empty(n_seqs, n_kv, budget, dtype=torch.int32, device=dev)
-    with _on(dev):
-        _check(lib.gptq_kv_evict(cache, seqs, weights.data_ptr(), ldw, budget, sinks, recent, new_pages.data_ptr(),
-                                 new_pages.stride(0) if n_seqs > 1 else new_pages.shape[1], table_out.data_ptr(),
-                                 max_pages, lens_out.data_ptr(), weights_out.data_ptr(), max_pages * ps,
-                                 kept.data_ptr(), torch.cuda.current_stream(dev).cuda_stream), "gptq_kv_evict")
+    # one allocation for the whole numbers: the kept slots, the table, the lengths
+    n_kept, n_table = n_seqs * n_kv * budget, n_seqs * max_pages
+    whole = torch.empty(n_kept + n_table + n_seqs, dtype=torch.int32, device=k.device)
+    kept = whole[:n_kept].view(n_seqs, n_kv, budget)
+    table_out = whole[n_kept:n_kept + n_table].view(n_seqs, max_pages)
+    lens_out = whole[n_kept + n_table:]
+    weights_out = torch.empty(n_seqs, n_kv, slots, dtype=torch.float32, device=k.device)
+    at = whole.data_ptr()
+    _launch(dev, lib.gptq_kv_evict, "gptq_kv_evict", cache, seqs, weights.data_ptr(), ldw, budget, sinks, recent,
+            new_pages.data_ptr(), new_pages.stride(0) if n_seqs > 1 else new_pages.shape[1], at + 4 * n_kept, max_pages,
+            at + 4 * (n_kept + n_table), weights_out.data_ptr(), slots, at)
     return table_out, lens_out, weights_out, kept
 
 
