@@ -23,30 +23,31 @@ __global__ __launch_bounds__(256) void append_kernel(KvView c, const uint4v* k_n
   const int64_t ld = (is_v ? ldv : ldk) >> 3;
   bf16_t* dst = (bf16_t*)(is_v ? c.v : c.k);  // 16-bit elements of either type
   const int cap = c.max_pages << c.page_shift;
+  // as stages without branches between, so that the loads of a stage are under way together
+  const int first = cu ? cu[0] : 0, last = cu ? cu[c.n_seqs] : n_tokens;
+  int b[TOK], page[TOK];
+  int64_t slot[TOK];
   uint4v x[TOK];
-  int64_t to[TOK];
 #pragma unroll
   for (int t = 0; t < TOK; ++t) {
-    to[t] = -1;
     const int i = blockIdx.x * TOK + t;
-    int first = 0, last = n_tokens;
-    if (cu) {
-      first = cu[0];
-      last = cu[c.n_seqs];
-    }
-    if (i >= n_tokens || i < first || i >= last) continue;
-    const int b = cu ? kv_seq_of(cu, c.n_seqs, i) : i;
-    const int n_b = cu ? cu[b + 1] - cu[b] : 1, at = cu ? i - cu[b] : 0;
-    const int64_t slot = (int64_t)c.lens[b] - n_b + at;
-    if (slot < 0 || slot >= cap) continue;
-    const int page = c.table[(int64_t)b * c.ld_table + (slot >> c.page_shift)];
-    if (!c.page_ok(page)) continue;
-    to[t] = c.head_base(page, h) + (slot & (c.page_size - 1)) * c.dim + off;
-    x[t] = src[(int64_t)i * ld + rc];
+    const bool in = i < n_tokens && i >= first && i < last;
+    x[t] = src[(int64_t)(i < n_tokens ? i : 0) * ld + rc];
+    b[t] = !in ? -1 : cu ? kv_seq_of(cu, c.n_seqs, i) : i;
+  }
+#pragma unroll
+  for (int t = 0; t < TOK; ++t) {
+    const int s = b[t] < 0 ? 0 : b[t];
+    slot[t] = (int64_t)c.lens[s] - (cu ? cu[s + 1] - (int64_t)(blockIdx.x * TOK + t) : 1);
+    if (b[t] < 0 || slot[t] < 0 || slot[t] >= cap) slot[t] = -1;
   }
 #pragma unroll
   for (int t = 0; t < TOK; ++t)
-    if (to[t] >= 0) *(uint4v*)(dst + to[t]) = x[t];
+    page[t] = c.table[(int64_t)(b[t] < 0 ? 0 : b[t]) * c.ld_table + ((slot[t] < 0 ? 0 : slot[t]) >> c.page_shift)];
+#pragma unroll
+  for (int t = 0; t < TOK; ++t)
+    if (slot[t] >= 0 && c.page_ok(page[t]))
+      *(uint4v*)(dst + c.head_base(page[t], h) + (slot[t] & (c.page_size - 1)) * c.dim + off) = x[t];
 }
 
 // Order-preserving key of a sum: larger weight, larger key; a NaN above all, and
@@ -58,6 +59,14 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 }
 
 constexpr int kSelThreads = 1024, kSelWaves = kSelThreads / 64, kBins = 2048;
+
+// x[0] + .. + x[wave - 1] (16 waves), by every lane.
+__device__ __forceinline__ uint32_t sum_before(const uint32_t* x, int wave) {
+  const int l = threadIdx.x & 15;
+  uint32_t v = l < wave ? x[l] : 0u;
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
 
 // Select: for one sequence and head, the slots that stay, in order. With
 // n > budget slots, the first `sinks` and the last `recent` stay, and of those
@@ -100,8 +109,7 @@ __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(KvView c, KvE
       }
       if (lane == 63) wave_sum[wave] = incl;
       __syncthreads();
-      uint32_t before = incl - h0 - h1;
-      for (int k = 0; k < wave; ++k) before += wave_sum[k];
+      const uint32_t before = incl - h0 - h1 + sum_before(wave_sum, wave);
       if (before < left && before + h0 >= left) {
         found_digit = kBins - 1 - 2 * tid;
         found_left = left - before;
@@ -139,11 +147,8 @@ __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(KvView c, KvE
     wave_eq[wave] = equal;
   }
   __syncthreads();
-  uint32_t sure_before = 0, eq_before = 0;
-  for (int k = 0; k < wave; ++k) {
-    sure_before += wave_sum[k];
-    eq_before += wave_eq[k];
-  }
+  const uint32_t sure_before = sum_before(wave_sum, wave);
+  uint32_t eq_before = sum_before(wave_eq, wave);
   uint32_t base = sure_before + (eq_before < left ? eq_before : left);
   const uint64_t below = lane == 0 ? 0ull : ~0ull >> (64 - lane);
   for (int r = t0; r < t1; r += 64) {
@@ -169,8 +174,7 @@ __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(KvView c, KvE
 
 // Move: the survivors' rows to the new pages, their sums to weights_out (zero
 // behind them), the table's row and the length. 16 lanes per row of up to 256
-// bytes, key and value together, kMoveRows rows per block, a thread's loads
-// before its stores. Source and destination pages are distinct, so every row
+// bytes, key and value together, kMoveRows rows per block. Source and destination pages are distinct, so every row
 // moves on its own.
 constexpr int kMoveRows = 64;
 
@@ -197,31 +201,38 @@ __global__ __launch_bounds__(256) void evict_move_kernel(KvView c, KvEvictArgs a
       a.table_out[(int64_t)b * a.ld_out + p] = !over ? row[p] : p < nd ? dst[p] : -1;
     if (tid == 0) a.lens_out[b] = left;
   }
-  if (!over) return;
+  if (!over || r0 >= a.budget) return;
   const int ch = tid & 15;
   if (ch * 8 >= c.dim) return;
+  // stage by stage over the thread's rows, without branches between: each stage's loads (the
+  // slot, its page, the row) are under way together (rows past the last repeat it, and a page
+  // that is none is read as page 0; neither is stored)
   constexpr int U = kMoveRows / 16;
-  uint4v xk[U], xv[U];
-  int64_t to[U];
+  int t[U], ps[U], pd[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    to[u] = -1;
-    const int i = r0 + u * 16 + (tid >> 4);
-    if (i >= a.budget) continue;
-    const int t = kept[i];
-    GPTQ_DASSERT(t >= 0 && t < n);
-    const int ps = row[t >> c.page_shift], pd = dst[i >> c.page_shift];
-    if (!c.page_ok(ps) || !c.page_ok(pd)) continue;
-    const int64_t from = c.head_base(ps, h) + (int64_t)(t & (c.page_size - 1)) * c.dim + ch * 8;
-    to[u] = c.head_base(pd, h) + (int64_t)(i & (c.page_size - 1)) * c.dim + ch * 8;
+    const int i = r0 + u * 16 + (tid >> 4), j = i < a.budget ? i : a.budget - 1;
+    t[u] = kept[j];
+    pd[u] = i < a.budget ? dst[j >> c.page_shift] : -1;
+    GPTQ_DASSERT(t[u] >= 0 && t[u] < n);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) ps[u] = row[t[u] >> c.page_shift];
+  uint4v xk[U], xv[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t from =
+        c.head_base(c.page_ok(ps[u]) ? ps[u] : 0, h) + (int64_t)(t[u] & (c.page_size - 1)) * c.dim + ch * 8;
     xk[u] = *(const uint4v*)((const bf16_t*)c.k + from);
     xv[u] = *(const uint4v*)((const bf16_t*)c.v + from);
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    if (to[u] < 0) continue;
-    *(uint4v*)((bf16_t*)c.k + to[u]) = xk[u];
-    *(uint4v*)((bf16_t*)c.v + to[u]) = xv[u];
+    if (!c.page_ok(ps[u]) || !c.page_ok(pd[u])) continue;
+    const int i = r0 + u * 16 + (tid >> 4);
+    const int64_t to = c.head_base(pd[u], h) + (int64_t)(i & (c.page_size - 1)) * c.dim + ch * 8;
+    *(uint4v*)((bf16_t*)c.k + to) = xk[u];
+    *(uint4v*)((bf16_t*)c.v + to) = xv[u];
   }
 }
 

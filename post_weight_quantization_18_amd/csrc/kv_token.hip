@@ -34,7 +34,7 @@ namespace gptq {
 namespace {
 
 constexpr int kTile = 32;     // slots per wave and step
-constexpr int kWaves = 4;     // waves per block
+constexpr int NW = 4;         // waves per block: 8 stream no faster (a compute unit's misses are the limit)
 constexpr float kRaise = 8.0f;  // in powers of two
 
 // The slots a token sees, as steps of kTile slots: the steps that hold sinks, then
@@ -55,6 +55,20 @@ struct Steps {
   __device__ __forceinline__ int slot0(int s) const { return (s < sink_steps ? s : s - sink_steps + jump) * kTile; }
 };
 
+// The i-th longest sequence (equal lengths in order), of up to 64; i itself of more. Blocks
+// start in order, and with the long sequences first the last ones to end are short.
+__device__ __forceinline__ int longest(const KvView& c, int i) {
+  if (c.n_seqs == 1 || c.n_seqs > 64) return i;
+  const int lane = threadIdx.x & 63;
+  const int n = lane < c.n_seqs ? c.len(lane) : -1;
+  int rank = 0;
+  for (int j = 0; j < c.n_seqs; ++j) {
+    const int m = __builtin_amdgcn_readlane(n, j);
+    rank += m > n || (m == n && j < lane);
+  }
+  return __builtin_ctzll(__ballot(rank == i && lane < c.n_seqs));
+}
+
 // Elements of the workspace (floats): per (sequence, head, split) the running
 // maximum, the sum and the unnormalized output; then the scores by step.
 struct TokenWs {
@@ -66,20 +80,20 @@ struct TokenWs {
 };
 
 // weights += 2^(score - m) / l, summed over the heads of a group, for the steps [s0,
-// s1) of one sequence and key head; sh holds m and 1 / l of each head. 256 threads, four
-// slots each at a time.
+// s1) of one sequence and key head; sh holds m and 1 / l of each head. Four slots per
+// thread at a time.
 __device__ __forceinline__ void add_weights(const KvView& c, const KvAttnArgs& a, const TokenWs& w, const Steps& st,
-                                            int b, int kvh, int s0, int s1, const float* sh) {
+                                            int b, int kvh, int s0, int s1, const float* sh, int threads) {
   const int group = a.n_heads / c.n_kv;
   const float* sp = w.scores + ((int64_t)b * a.n_heads + kvh * group) * w.n_scores;
   float* wt = a.weights + ((int64_t)b * c.n_kv + kvh) * a.ldw;
   const int end = (s1 < st.total ? s1 : st.total) * kTile;
-  for (int k0 = s0 * kTile + threadIdx.x; k0 < end; k0 += 1024) {
+  for (int k0 = s0 * kTile + threadIdx.x; k0 < end; k0 += 4 * threads) {
     float add[4] = {0, 0, 0, 0}, old[4];
     int t[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int k = k0 + 256 * i;
+      const int k = k0 + threads * i;
       t[i] = -1;
       if (k < end) {
         const int slot = st.slot0(k / kTile) + k % kTile;
@@ -91,7 +105,7 @@ __device__ __forceinline__ void add_weights(const KvView& c, const KvAttnArgs& a
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (t[i] >= 0)
-          add[i] += __builtin_amdgcn_exp2f(sp[(int64_t)h * w.n_scores + k0 + 256 * i] - sh[2 * h]) * sh[2 * h + 1];
+          add[i] += __builtin_amdgcn_exp2f(sp[(int64_t)h * w.n_scores + k0 + threads * i] - sh[2 * h]) * sh[2 * h + 1];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (t[i] >= 0) wt[t[i]] = old[i] + add[i];
@@ -108,7 +122,7 @@ struct TokenRegs {
 // (16 VEC >= dim). SPLIT: partial results to the workspace. SCORES: the
 // stored too.
 template <typename T, int KS, int VEC, bool SPLIT, bool SCORES>
-__global__ __launch_bounds__(64 * kWaves, 2) void token_kernel(KvView c, KvAttnArgs a, TokenWs w) {
+__global__ __launch_bounds__(64 * NW, 2) void token_kernel(KvView c, KvAttnArgs a, TokenWs w) {
   using KT = KvType<T>;
   using x8 = typename KT::x8;
   const int lane = threadIdx.x & 63, g = lane >> 4, cl = lane & 15;
@@ -119,7 +133,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void token_kernel(KvView c, KvAttnA
   id /= w.n_splits;
   const int h0 = (id % qt) * 16;
   id /= qt;
-  const int kvh = id % c.n_kv, b = id / c.n_kv;
+  const int kvh = id % c.n_kv, b = longest(c, id / c.n_kv);
   const int n_h = group - h0 < 16 ? group - h0 : 16;
   const int head = kvh * group + h0 + (cl < n_h ? cl : 0);  // this lane's column
 
@@ -271,24 +285,28 @@ __global__ __launch_bounds__(64 * kWaves, 2) void token_kernel(KvView c, KvAttnA
   Regs ra, rb;
   int s = split * per + wave;
   if (s < s_end) {
-    Pages pa = pages(s), pb = pages(s + kWaves);
+    Pages pa = pages(s), pb = pages(s + NW);
     load(s, pa, ra);
     while (true) {
-      // the next step's rows (the last step loads itself again, unused)
-      const bool more = s + kWaves < s_end;
-      load(more ? s + kWaves : s, more ? pb : pa, rb);
-      Pages pc = pages(s + 2 * kWaves);
+      // Page numbers two steps ahead, then the next step's rows (the last step loads itself
+      // again, unused). In this order: loads return in order, and a wait for the page numbers
+      // must not be one for the rows behind them.
+      const bool more = s + NW < s_end;
+      const Pages pc = pages(s + 2 * NW);
+      asm volatile("" ::: "memory");
+      load(more ? s + NW : s, more ? pb : pa, rb);
       asm volatile("" ::: "memory");
       compute(s, pa, ra);
       if (!more) break;
-      s += kWaves;
-      const bool more2 = s + kWaves < s_end;
-      load(more2 ? s + kWaves : s, more2 ? pc : pb, ra);
-      Pages pd = pages(s + 2 * kWaves);
+      s += NW;
+      const bool more2 = s + NW < s_end;
+      const Pages pd = pages(s + 2 * NW);
+      asm volatile("" ::: "memory");
+      load(more2 ? s + NW : s, more2 ? pc : pb, ra);
       asm volatile("" ::: "memory");
       compute(s, pb, rb);
       if (!more2) break;
-      s += kWaves;
+      s += NW;
       pa = pc;
       pb = pd;
     }
@@ -297,8 +315,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void token_kernel(KvView c, KvAttnA
   // join the waves of the block
   lsum += __shfl_xor(lsum, 16);
   lsum += __shfl_xor(lsum, 32);
-  __shared__ float sm[kWaves][16], sl[kWaves][16], fin[32];
-  __shared__ float so[kWaves][16][16 * VEC + 4];
+  __shared__ float sm[NW][16], sl[NW][16], fin[32];
+  constexpr int kPitch = 16 * VEC + 4;
+  extern __shared__ __attribute__((aligned(16))) float so[];  // [NW][n_h][kPitch]
   if (g == 0) {
     sm[wave][cl] = m;
     sl[wave][cl] = lsum;
@@ -307,21 +326,21 @@ __global__ __launch_bounds__(64 * kWaves, 2) void token_kernel(KvView c, KvAttnA
 #pragma unroll
     for (int i = 0; i < VEC; ++i)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) so[wave][cl][(4 * g + r) * VEC + i] = o[i][r];
+      for (int r = 0; r < 4; ++r) so[(wave * n_h + cl) * kPitch + (4 * g + r) * VEC + i] = o[i][r];
   }
   __syncthreads();
-  for (int k = threadIdx.x; k < n_h * c.dim; k += 64 * kWaves) {
+  for (int k = threadIdx.x; k < n_h * c.dim; k += 64 * NW) {
     const int hh = k / c.dim, e = k - hh * c.dim;
     float mm = -INFINITY;
 #pragma unroll
-    for (int u = 0; u < kWaves; ++u) mm = fmaxf(mm, sm[u][hh]);
+    for (int u = 0; u < NW; ++u) mm = fmaxf(mm, sm[u][hh]);
     float l = 0.0f, v = 0.0f;
 #pragma unroll
-    for (int u = 0; u < kWaves; ++u) {
+    for (int u = 0; u < NW; ++u) {
       const float f = sm[u][hh] == -INFINITY ? 0.0f : exp2f(sm[u][hh] - mm);
       // a wave without a visible slot holds zeros
       l += f * sl[u][hh];
-      v += f * so[u][hh][e];
+      v += f * so[(u * n_h + hh) * kPitch + e];
     }
     const int64_t bh = (int64_t)b * a.n_heads + kvh * group + h0 + hh;
     if constexpr (SPLIT) {
@@ -341,7 +360,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void token_kernel(KvView c, KvAttnA
   if constexpr (SCORES && !SPLIT) {
     // this block has seen all scores of its key head: its own writes, read back
     __syncthreads();
-    add_weights(c, a, w, st, b, kvh, 0, st.total, fin);
+    add_weights(c, a, w, st, b, kvh, 0, st.total, fin, 64 * NW);
   }
 }
 
@@ -410,7 +429,7 @@ __global__ __launch_bounds__(256) void token_join_kernel(KvView c, KvAttnArgs a,
     }
   }
   __syncthreads();
-  add_weights(c, a, w, st, b, kvh, part * kJoinSteps, (part + 1) * kJoinSteps, sh);
+  add_weights(c, a, w, st, b, kvh, part * kJoinSteps, (part + 1) * kJoinSteps, sh, 256);
 }
 
 int64_t max_steps(const KvView& c, int64_t window, int64_t sinks) {
@@ -420,14 +439,22 @@ int64_t max_steps(const KvView& c, int64_t window, int64_t sinks) {
   return some < all ? some : all;
 }
 
-// Blocks per (sequence, key head, tile of heads).
+// Blocks per (sequence, key head, tile of heads). One compute unit streams about 45
+// GB/s, so a call that has fewer blocks than there are compute units splits its
+// sequences until there is one each: a sequence of 2048 slots and 8 key heads takes
+// 23.8 us unsplit, 9.8 split by 16. Sequences of different lengths get twice as many
+// where that is many (three of 9001 to 32768 slots: 62.9 us at 10 splits each, 57.5 at
+// 21; eight of one length 27.3 and 27.6). A block of up to 256 KB stays whole, since the
+// second kernel costs more than splitting gives (300 slots of 80, 32 key heads: 7.0 us
+// whole, 9.0 split by 2), and so do more pairs than half the compute units (160 of 2048
+// slots: 28.3 us whole, 35.4 split by 2).
 int64_t splits_of(const KvView& c, int64_t n_heads, int64_t window, int64_t sinks) {
   const int64_t base = (int64_t)c.n_seqs * c.n_kv * ceil_div(n_heads / c.n_kv, 16);
-  const int64_t most = ceil_div(max_steps(c, window, sinks), kWaves);
-  int64_t s = ceil_div(1024, base);
-  if (s > most) s = most;
-  if (s > 256) s = 256;
-  return s < 1 ? 1 : s;
+  const int64_t steps = max_steps(c, window, sinks);
+  if (steps * kTile * c.dim * 4 <= (256 << 10)) return 1;
+  int64_t s = 256 / base;
+  if (c.n_seqs > 1 && s >= 4) s = 512 / base;
+  return std::max<int64_t>(1, std::min<int64_t>(s, ceil_div(steps, NW)));
 }
 
 TokenWs layout(const KvView& c, int64_t n_heads, int64_t window, int64_t sinks, bool weights, void* ws, size_t* bytes) {
@@ -436,14 +463,14 @@ TokenWs layout(const KvView& c, int64_t n_heads, int64_t window, int64_t sinks, 
   w.join = w.n_splits > 1 || (weights && n_heads / c.n_kv > 16);
   w.n_scores = (int)(max_steps(c, window, sinks) * kTile);
   const int64_t rows = (int64_t)c.n_seqs * n_heads;
-  float* p = (float*)ws;
+  float* f = (float*)ws;
   size_t n = 0;
-  w.scores = p;  // multiples of 4 floats each: all 16-byte aligned
+  w.scores = f;  // multiples of 4 floats each: all 16-byte aligned
   if (weights) n += (size_t)rows * w.n_scores;
   if (w.join) {
-    w.o = p + n;
+    w.o = f + n;
     n += (size_t)rows * w.n_splits * c.dim;
-    w.ml = p + n;
+    w.ml = f + n;
     n += (size_t)rows * w.n_splits * 2;
   }
   if (bytes) *bytes = n * sizeof(float);
@@ -452,17 +479,19 @@ TokenWs layout(const KvView& c, int64_t n_heads, int64_t window, int64_t sinks, 
 
 template <typename T, int KS, int VEC>
 gptq_status_t launch(const KvView& c, const KvAttnArgs& a, const TokenWs& w, hipStream_t st) {
-  const int64_t blocks = (int64_t)c.n_seqs * c.n_kv * ceil_div(a.n_heads / c.n_kv, 16) * w.n_splits;
-  if (blocks * 64 * kWaves >= (int64_t)1 << 32) return GPTQ_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)blocks), blk(64 * kWaves);
+  const int64_t group = a.n_heads / c.n_kv;
+  const int64_t blocks = (int64_t)c.n_seqs * c.n_kv * ceil_div(group, 16) * w.n_splits;
+  if (blocks * 64 * NW >= (int64_t)1 << 32) return GPTQ_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)blocks), blk(64 * NW);
+  const size_t lds = NW * (size_t)std::min<int64_t>(group, 16) * (16 * VEC + 4) * sizeof(float);
   if (a.weights && w.join)
-    hipLaunchKernelGGL((token_kernel<T, KS, VEC, true, true>), grid, blk, 0, st, c, a, w);
+    hipLaunchKernelGGL((token_kernel<T, KS, VEC, true, true>), grid, blk, lds, st, c, a, w);
   else if (a.weights)
-    hipLaunchKernelGGL((token_kernel<T, KS, VEC, false, true>), grid, blk, 0, st, c, a, w);
+    hipLaunchKernelGGL((token_kernel<T, KS, VEC, false, true>), grid, blk, lds, st, c, a, w);
   else if (w.join)
-    hipLaunchKernelGGL((token_kernel<T, KS, VEC, true, false>), grid, blk, 0, st, c, a, w);
+    hipLaunchKernelGGL((token_kernel<T, KS, VEC, true, false>), grid, blk, lds, st, c, a, w);
   else
-    hipLaunchKernelGGL((token_kernel<T, KS, VEC, false, false>), grid, blk, 0, st, c, a, w);
+    hipLaunchKernelGGL((token_kernel<T, KS, VEC, false, false>), grid, blk, lds, st, c, a, w);
   GPTQ_CHECK_LAUNCH();
   return GPTQ_OK;
 }
@@ -473,13 +502,9 @@ gptq_status_t token_enqueue(const KvView& c, const KvAttnArgs& a, void* ws, hipS
   const int64_t parts = a.weights ? ceil_div(w.n_scores / kTile, kJoinSteps) : 1;
   const int64_t jblocks = (int64_t)c.n_seqs * (a.n_heads + (a.weights ? c.n_kv * parts : 0));
   if (jblocks * 256 >= (int64_t)1 << 32) return GPTQ_ERR_UNSUPPORTED;
-  gptq_status_t rc;
-  if (c.dim <= 64)
-    rc = launch<T, 2, 4>(c, a, w, st);
-  else if (c.dim <= 96)
-    rc = launch<T, 3, 8>(c, a, w, st);
-  else
-    rc = launch<T, 4, 8>(c, a, w, st);
+  const gptq_status_t rc = c.dim <= 64   ? launch<T, 2, 4>(c, a, w, st)
+                           : c.dim <= 96 ? launch<T, 3, 8>(c, a, w, st)
+                                         : launch<T, 4, 8>(c, a, w, st);
   if (rc != GPTQ_OK || !w.join) return rc;
   hipLaunchKernelGGL(token_join_kernel<T>, dim3((unsigned)jblocks), dim3(256),
                      std::max<size_t>(4096, 2 * sizeof(float) * (a.n_heads / c.n_kv)), st, c, a, w, (int)parts);
