@@ -73,11 +73,11 @@ def test_append_refusals(lib):
 
 
 def _attend(lib, prompt, q=P, ldq=256, heads=4, scale=0.125, window=0, sinks=0, w=None, ldw=0, out=P << 1, ldo=256,
-            ws=P, nbytes=1 << 30, cu=P, n=9):
+            ws=P, nbytes=1 << 30, cu=P, n=9, **seqs):
     if prompt:
-        return lib.gptq_paged_prefill(_cache(), _seqs(), q, ldq, cu, n, heads, scale, window, sinks, w, ldw, out, ldo,
+        return lib.gptq_paged_prefill(_cache(), _seqs(**seqs), q, ldq, cu, n, heads, scale, window, sinks, w, ldw, out, ldo,
                                       ws, nbytes, None)
-    return lib.gptq_paged_attention(_cache(), _seqs(), q, ldq, heads, scale, window, sinks, w, ldw, out, ldo, ws,
+    return lib.gptq_paged_attention(_cache(), _seqs(**seqs), q, ldq, heads, scale, window, sinks, w, ldw, out, ldo, ws,
                                     nbytes, None)
 
 
@@ -94,9 +94,10 @@ def test_attention_refusals(lib, prompt):
         assert call(scale=s) == BAD
     assert call(window=-1) == BAD and call(sinks=-1) == BAD
     assert call(w=P, ldw=63) == BAD and call(w=P + 2, ldw=64) == BAD
-    assert call(w=P, ldw=64, ws=None, nbytes=0) == WS
-    assert call(w=P, ldw=64, nbytes=16) == WS
-    assert call(w=P, ldw=64, ws=P + 64) == WS
+    long = dict(w=P, ldw=65536, max_pages=4096, ld_table=4096)                # too long for one block's LDS
+    assert call(ws=None, nbytes=0, **long) == WS
+    assert call(nbytes=16, **long) == WS
+    assert call(ws=P + 64, **long) == WS
     if prompt:
         assert call(cu=None) == BAD and call(n=-1) == BAD and call(n=1 << 30) == BAD
         assert call(out=P) == BAD                                            # in place
@@ -121,11 +122,11 @@ def test_workspace_sizes(lib):
     def size(window=0, sinks=0, n=0, w=0, heads=4, **kw):
         return lib.gptq_kv_workspace_bytes(_cache(), _seqs(**kw), heads, window, sinks, n, w)
     assert size(n=9) == 0 and size(n=9, w=1) == 9 * 4 * 4                    # a prompt's row normalizers
+    assert size(w=1) == 0 and size() == 0                                    # one block a key head, its scores in LDS
     # a token's scores: every visible slot of every head
-    assert size(w=1) >= 3 * 4 * 64 * 4
-    # a window bounds them, whatever the capacity
     big = dict(max_pages=4096, ld_table=4096)
     assert size(w=1, **big) >= 3 * 4 * 65536 * 4
+    # a window bounds them, whatever the capacity
     assert size(w=1, window=100, sinks=4, **big) < size(w=1, **big) / 8
     assert size(heads=3) == 0 and size(window=-1) == 0 and size(n=-1) == 0
 
