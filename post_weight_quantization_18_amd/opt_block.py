@@ -26,6 +26,11 @@ LayerNorm gain 1 and shift 0). Layers and their calibration inputs:
 Products take fp16 operands with fp32 accumulation; LayerNorm, the attention
 scores and the softmax are fp32; activations are stored in fp16, the dtype
 the Hessian accumulation takes.
+
+GenerationBlock then generates through the quantized block: prompts with the
+dequantized weights, single tokens with the packed ones (gptq_dequant_gemv), the
+attention of both over a paged key-value cache (gptq_kv_append,
+gptq_paged_prefill, gptq_paged_attention), which gptq_kv_evict keeps to a budget.
 """
 
 from __future__ import annotations
@@ -196,3 +201,109 @@ class SequentialBlock:
         self.stage_s = {"forward_ms": el[0] + el[2] + el[4] + el[6],
                         "quantize_ms": {"qkv": el[1], "out": el[3], "fc1": el[5], "fc2": el[7]}}
         return y
+
+
+class GenerationBlock:
+    """Generation through one quantized block for n_seqs sequences that share a paged
+    key-value cache. `results` holds the six sublayers' quantize_layer outputs
+    (SequentialBlock.results); w_hat is needed for prompts only.
+
+    prompt(x, lens)   the first tokens of every sequence (or more of them)
+    token(x)          one token of every sequence
+    With budget > 0 the attention weights of every slot are accumulated, and once a
+    sequence holds more than budget + slack slots it falls back to budget: its first
+    `sinks`, its last `recent` and the most attended others stay. With window > 0
+    a token sees the last `window` slots and the first `sinks`.
+    Pages are taken from a free list as sequences grow, and given back by eviction."""
+
+    def __init__(self, shape: BlockShape, results, n_seqs: int, max_len: int, page_size: int = 64, window: int = 0,
+                 sinks: int = 0, budget: int = 0, recent: int = 0, slack: int = 0):
+        if budget and budget + slack > max_len:
+            raise ValueError("budget + slack must not exceed max_len")
+        self.shape, self.results, self.n_seqs, self.page_size = shape, results, n_seqs, page_size
+        self.window, self.sinks, self.budget, self.recent, self.slack = window, sinks, budget, recent, slack
+        self.device = results["q"]["qcodes"].device
+        self.head_dim = shape.d_model // shape.n_heads
+        self.max_pages = -(-max_len // page_size)
+        spare = -(-budget // page_size) if budget else 0  # an evicted sequence's new pages, beside its old ones
+        n_pages = n_seqs * (self.max_pages + spare)
+        self.k = torch.zeros(n_pages, shape.n_heads, page_size, self.head_dim, dtype=torch.float16, device=self.device)
+        self.v = torch.zeros_like(self.k)
+        self.table = torch.full((n_seqs, self.max_pages), -1, dtype=torch.int32, device=self.device)
+        self.lens = [0] * n_seqs
+        self.pages = [[] for _ in range(n_seqs)]
+        self.free = list(range(n_pages))
+        self.weights = torch.zeros(n_seqs, shape.n_heads, self.max_pages * page_size, dtype=torch.float32,
+                                   device=self.device) if budget else None
+        self.kept = None  # the last eviction's old slot of every new one
+
+    def _grow(self, new):
+        """Room for new[b] more slots of every sequence; returns lens on the device."""
+        for b, n in enumerate(new):
+            if self.lens[b] + n > self.max_pages * self.page_size:
+                raise ValueError(f"sequence {b} outgrows the cache ({self.lens[b]} + {n} slots)")
+        for b, n in enumerate(new):
+            self.lens[b] += n
+            have, need = len(self.pages[b]), -(-self.lens[b] // self.page_size)
+            if need > have:
+                more = [self.free.pop() for _ in range(need - have)]
+                self.pages[b] += more
+                self.table[b, have:need] = torch.tensor(more, dtype=torch.int32, device=self.device)
+        return torch.tensor(self.lens, dtype=torch.int32, device=self.device)
+
+    def _heads(self, t):
+        return t.view(t.shape[0], self.shape.n_heads, self.head_dim)
+
+    def _finish(self, x, o, product):
+        """The block behind its attention: out, residual, fc1, ReLU, fc2, residual."""
+        h = (x.float() + product("out", o).float()).half()
+        u = torch.relu(product("fc1", layer_norm(h)))
+        return (h.float() + product("fc2", u).float()).half()
+
+    def prompt(self, x: torch.Tensor, lens) -> torch.Tensor:
+        """x fp16 [sum(lens), d_model]: lens[b] tokens of every sequence b, one after the
+        other. Returns the block's output rows."""
+        def product(name, t):
+            return linear(t, self.results[name]["w_hat"])
+
+        dev_lens = self._grow(lens)
+        cu = torch.tensor([0, *lens], dtype=torch.int32).cumsum(0, dtype=torch.int32).to(self.device)
+        a = layer_norm(x)
+        q, k, v = (self._heads(product(n, a)) for n in ("q", "k", "v"))
+        G.kv_append(self.k, self.v, self.table, dev_lens, k, v, cu)
+        o = G.paged_prefill(q, self.k, self.v, self.table, dev_lens, cu, window=self.window, sinks=self.sinks,
+                            weights=self.weights)
+        y = self._finish(x, o.view(x.shape[0], -1), product)
+        self._evict(dev_lens)
+        return y
+
+    def token(self, x: torch.Tensor) -> torch.Tensor:
+        """x fp16 [n_seqs, d_model], one token of every sequence. Returns the block's output rows."""
+        def product(name, t):
+            r, bits, group = self.results[name], self.shape.bits, self.shape.group
+            return torch.stack([G.dequant_gemv(r["qcodes"], r["scales"], r["zeros"], bits, group, row) for row in
+                                t.contiguous()]).half()
+
+        dev_lens = self._grow([1] * self.n_seqs)
+        a = layer_norm(x)
+        q, k, v = (self._heads(product(n, a)) for n in ("q", "k", "v"))
+        G.kv_append(self.k, self.v, self.table, dev_lens, k, v)
+        o = G.paged_attention(q, self.k, self.v, self.table, dev_lens, window=self.window, sinks=self.sinks,
+                              weights=self.weights)
+        y = self._finish(x, o.view(x.shape[0], -1), product)
+        self._evict(dev_lens)
+        return y
+
+    def _evict(self, dev_lens):
+        if not self.budget or max(self.lens) <= self.budget + self.slack:
+            return
+        over = [b for b in range(self.n_seqs) if self.lens[b] > self.budget]
+        per = -(-self.budget // self.page_size)
+        new = [[self.free.pop() for _ in range(per)] if b in over else [-1] * per for b in range(self.n_seqs)]
+        into = torch.tensor(new, dtype=torch.int32, device=self.device)
+        self.table, _, self.weights, self.kept = G.kv_evict(self.k, self.v, self.table, dev_lens, self.weights,
+                                                            self.budget, into, sinks=self.sinks, recent=self.recent)
+        for b in over:
+            self.free += self.pages[b]
+            self.pages[b] = new[b]
+            self.lens[b] = self.budget
