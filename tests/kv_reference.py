@@ -41,7 +41,7 @@ def attend(q, k, v, there, p, scale, window, sinks, u_p, u_out):
         g = h // group
         kk, vv = k[g, idx], v[g, idx]
         s = scale * (kk @ q[h])
-        mass = scale * (np.abs(kk) @ np.abs(q[h]))
+        mass = abs(scale) * (np.abs(kk) @ np.abs(q[h]))
         w = np.exp(s - s.max())
         w /= w.sum()
         d_s = dim * U * mass.max() + 8 * U * max(1.0, np.abs(s).max())

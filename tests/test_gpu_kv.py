@@ -97,6 +97,8 @@ TOKEN = [
     ("fp16", [90, 200], 2, 2, 8, 16, 17, 500),
     ("bf16", [1025], 2, 2, 128, 256, 7, 1),
     ("fp16", [2300, 700], 1, 1, 128, 64, 0, 0),        # many splits
+    ("fp16", [9000], 256, 256, 8, 256, 0, 0),          # whole, scores too many for LDS
+    ("bf16", [2100, 40, 0], 34, 2, 64, 32, 1500, 3),   # 17 heads a key, splits and a window
 ]
 
 
@@ -138,6 +140,9 @@ PROMPT = [
     ("fp16", [400], [200], 1, 1, 128, 128, 100, 130),
     ("fp16", [150, 90], [150, 90], 2, 2, 24, 8, 17, 70),
     ("bf16", [129, 5], [129, 5], 7, 1, 40, 16, 0, 0),
+    ("fp16", [1200], [130], 2, 1, 128, 16, 0, 0),       # more tiles than page numbers held at once
+    ("bf16", [1500, 700], [300, 2], 2, 2, 64, 64, 700, 5),
+    ("fp16", [600, 580], [600, 580], 1, 1, 80, 8, 64, 100),
     ("fp16", [3, 20], [10, 25], 2, 2, 64, 8, 0, 0),     # more new tokens than slots: rows that see nothing
 ]
 
@@ -394,3 +399,157 @@ def test_evict(case):
                     c.v[into[b, i // ps], h, i % ps] = c.v[c.table[b, t // ps], h, t % ps]
     assert torch.equal(k.cpu().view(torch.int16), c.k.view(torch.int16))
     assert torch.equal(v.cpu().view(torch.int16), c.v.view(torch.int16))
+
+
+def test_scales():
+    """A scale of its own, also zero (equal weights) and negative."""
+    c = Case("fp16", [77, 40], 4, 2, 64, 16)
+    q = c.queries(2)
+    k, v, table, ln = c.gpu()
+    cu = torch.tensor([0, 1, 2], dtype=torch.int32, device=DEV)
+    for scale in (0.0, 0.7, -0.125, 1e-4):
+        print(f"[case] scale {scale}", flush=True)
+        want, tol, added, wtol = c.expect(q, [0, 1, 2], 0, 0, 2.0 ** -11, scale=scale)
+        for prompt in (False, True):
+            wd = torch.zeros(2, 2, table.shape[1] * 16, device=DEV)
+            if prompt:
+                out = G.paged_prefill(q.to(DEV), k, v, table, ln, cu, scale=scale, weights=wd)
+            else:
+                out = G.paged_attention(q.to(DEV), k, v, table, ln, scale=scale, weights=wd)
+            _near(out, want, tol, f"scale {scale} prompt {prompt}")
+            _near(wd, added, wtol + 4 * R.U, f"weights, scale {scale} prompt {prompt}")
+
+
+def test_output_in_place_of_the_queries_and_the_same_bits_every_time():
+    print("[case] in place, repeated", flush=True)
+    for lens, heads, kv in (([300, 40], 4, 4), ([3000], 4, 1)):   # whole and split
+        c = Case("fp16", lens, heads, kv, 128, 16)
+        q = c.queries(len(lens)).to(DEV)
+        k, v, table, ln = c.gpu()
+        w = [torch.zeros(len(lens), kv, table.shape[1] * 16, device=DEV) for _ in range(3)]
+        first = G.paged_attention(q, k, v, table, ln, weights=w[0])
+        assert torch.equal(first, G.paged_attention(q, k, v, table, ln, weights=w[1])) and torch.equal(w[0], w[1])
+        cu = torch.arange(len(lens) + 1, dtype=torch.int32, device=DEV)
+        a = G.paged_prefill(q, k, v, table, ln, cu, weights=w[1].zero_())
+        assert torch.equal(a, G.paged_prefill(q, k, v, table, ln, cu, weights=w[2])) and torch.equal(w[1], w[2])
+        G.paged_attention(q, k, v, table, ln, out=q)
+        assert torch.equal(q, first)
+
+
+def _step(k, v, table, ln, new, q, w, ws, out):
+    """One decode step as a graph holds it: the lengths grow on the device."""
+    ln.add_(1)
+    G.kv_append(k, v, table, ln, new, new)
+    G.paged_attention(q, k, v, table, ln, weights=w, out=out, workspace=ws)
+
+
+def test_captured_steps_replay_with_the_lengths_of_the_moment():
+    print("[case] graph of a decode step", flush=True)
+    c = Case("fp16", [1100, 30], 8, 2, 128, 16, max_pages=80)
+    c.table[:, :] = 0
+    g = torch.Generator().manual_seed(3)
+    table = torch.randperm(160, generator=g).to(torch.int32).view(2, 80).to(DEV)
+    k = torch.randn(160, 2, 16, 128, generator=g).half().to(DEV)
+    v = torch.randn(160, 2, 16, 128, generator=g).half().to(DEV)
+    q = torch.randn(2, 8, 128, generator=g).half().to(DEV)
+    new = torch.randn(2, 2, 128, generator=g).half().to(DEV)
+    start = torch.tensor([1100, 30], dtype=torch.int32, device=DEV)
+    size = max(256, G.kv_workspace_bytes(k, v, table, start, 8, weights=True))
+
+    def state():
+        return [k.clone(), v.clone(), start.clone(), torch.zeros(2, 2, 80 * 16, device=DEV),
+                torch.empty(size, dtype=torch.uint8, device=DEV), torch.empty_like(q)]
+
+    eager = state()
+    want = []
+    for _ in range(5):
+        _step(eager[0], eager[1], table, eager[2], new, q, eager[3], eager[4], eager[5])
+        want.append([x.clone() for x in (eager[0], eager[1], eager[2], eager[3], eager[5])])
+    torch.cuda.synchronize()
+    s = state()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):   # (kernels loaded before the capture)
+        _step(s[0].clone(), s[1].clone(), table, s[2].clone(), new, q, s[3].clone(), s[4], s[5])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _step(s[0], s[1], table, s[2], new, q, s[3], s[4], s[5])
+    for i in range(5):
+        graph.replay()
+        if i % 2:   # the program's own eager work between replays
+            G.paged_attention(q, k, v, table, start)
+            torch.cuda.synchronize()
+        for a, b in zip(want[i], (s[0], s[1], s[2], s[3], s[5])):
+            assert torch.equal(a, b), i
+
+
+def test_captured_prompt_and_eviction():
+    print("[case] graph of a prompt and an eviction", flush=True)
+    c = Case("bf16", [200, 150], 4, 2, 64, 16, spare=20)
+    q = c.queries(100).to(DEV)
+    k, v, table, ln = c.gpu()
+    cu = torch.tensor([0, 60, 100], dtype=torch.int32, device=DEV)
+    into = torch.tensor(c.free[:8], dtype=torch.int32, device=DEV).view(2, 4)
+    w = torch.zeros(2, 2, table.shape[1] * 16, device=DEV)
+
+    def run():
+        w.zero_()
+        out = G.paged_prefill(q, k, v, table, ln, cu, weights=w, window=90, sinks=3)
+        return [out, *G.kv_evict(k, v, table, ln, w, 64, into, sinks=3, recent=20)]
+
+    want = [x.clone() for x in run()]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    for _ in range(4):
+        for x in got:
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert torch.equal(a, b)
+
+
+def test_calls_on_two_streams_at_once():
+    """Two batches on two streams, each with its own workspace, give what each gives alone."""
+    print("[case] two streams", flush=True)
+    cases = [Case("fp16", [1500, 33], 8, 2, 128, 16, seed=s) for s in (1, 2)]
+    data = [(c.queries(2).to(DEV), *c.gpu()) for c in cases]
+    alone = [G.paged_attention(*d) for d in data]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(G.paged_attention(*data[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(alone[i], x) for x in got[i])
+
+
+def test_trace_names_the_cache_kernels():
+    c = Case("fp16", [50], 2, 2, 64, 16, spare=6)
+    k, v, table, ln = c.gpu()
+    q = c.queries(1).to(DEV)
+    w = torch.zeros(1, 2, table.shape[1] * 16, device=DEV)
+    G.trace_start()
+    G.kv_append(k, v, table, ln, q, q)
+    G.paged_attention(q, k, v, table, ln, weights=w)
+    G.paged_prefill(q, k, v, table, ln, torch.tensor([0, 1], dtype=torch.int32, device=DEV))
+    G.kv_evict(k, v, table, ln, w, 30, torch.tensor([c.free[:2]], dtype=torch.int32, device=DEV))
+    torch.cuda.synchronize()
+    fam = G.trace_stop()
+    assert fam["kv_append"]["launches"] == 1 and fam["kv_attention"]["launches"] == 2 and fam["kv_evict"]["launches"] == 1
+    assert all(f["ms"] > 0 for f in fam.values())
+
+
+def test_a_tensor_of_another_device_is_refused():
+    c = Case("fp16", [50], 2, 2, 64, 16)
+    k, v, table, ln = c.gpu()
+    q = c.queries(1)
+    with pytest.raises(ValueError, match="device"):
+        G.paged_attention(q, k, v, table, ln)
+    with pytest.raises(ValueError, match="device"):
+        G.kv_append(k, v, table, ln.cpu(), q.to(DEV), q.to(DEV))
