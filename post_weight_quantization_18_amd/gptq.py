@@ -431,12 +431,11 @@ def _kv(k, v, page_table, lens):
         raise ValueError("k and v: equal strides, contiguous within a page")
     if page_table.dtype != torch.int32 or lens.dtype != torch.int32:
         raise ValueError("page_table and lens must be int32")
-    if page_table.dim() != 2 or lens.dim() != 1:
+    rows = page_table.shape
+    if len(rows) != 2 or lens.shape != rows[:1]:
         raise ValueError("page_table [n_seqs, max_pages], lens [n_seqs]")
-    n_seqs, max_pages = page_table.shape
+    n_seqs, max_pages = rows
     ld, one = page_table.stride()
-    if lens.shape[0] != n_seqs:
-        raise ValueError("page_table [n_seqs, max_pages], lens [n_seqs]")
     if (one != 1 and max_pages > 1) or (n_seqs > 1 and lens.stride(0) != 1):
         raise ValueError("page_table rows and lens must be contiguous")
     # the stride of a single page or row says nothing
@@ -483,11 +482,12 @@ def _weights(w, name, n_seqs, n_kv, slots):
 
 def _launch(dev, fn, what, *args):
     """fn(*args, stream) on device dev and its current stream."""
+    # (the raw handle: a Stream object around it costs a microsecond)
     if torch.cuda.current_device() == dev:
-        status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     if status:
         raise GPTQError(status, what)
 
@@ -603,17 +603,13 @@ def kv_evict(k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, lens: t
         raise ValueError("new_pages must be int32 [n_seqs, pages], rows contiguous")
     if budget < 1:
         raise ValueError("budget must be positive")
-    # one allocation for the whole numbers: the kept slots, the table, the lengths
-    n_kept, n_table = n_seqs * n_kv * budget, n_seqs * max_pages
-    whole = torch.empty(n_kept + n_table + n_seqs, dtype=torch.int32, device=k.device)
-    kept = whole[:n_kept].view(n_seqs, n_kv, budget)
-    table_out = whole[n_kept:n_kept + n_table].view(n_seqs, max_pages)
-    lens_out = whole[n_kept + n_table:]
-    weights_out = torch.empty(n_seqs, n_kv, slots, dtype=torch.float32, device=k.device)
-    at = whole.data_ptr()
+    table_out = torch.empty_like(page_table, memory_format=torch.contiguous_format)
+    lens_out = torch.empty_like(lens)
+    weights_out = torch.empty_like(weights)
+    kept = torch.empty(n_seqs, n_kv, budget, dtype=torch.int32, device=k.device)
     _launch(dev, lib.gptq_kv_evict, "gptq_kv_evict", cache, seqs, weights.data_ptr(), ldw, budget, sinks, recent,
-            new_pages.data_ptr(), new_pages.stride(0) if n_seqs > 1 else new_pages.shape[1], at + 4 * n_kept, max_pages,
-            at + 4 * (n_kept + n_table), weights_out.data_ptr(), slots, at)
+            new_pages.data_ptr(), new_pages.stride(0) if n_seqs > 1 else new_pages.shape[1], table_out.data_ptr(),
+            max_pages, lens_out.data_ptr(), weights_out.data_ptr(), ldw, kept.data_ptr())
     return table_out, lens_out, weights_out, kept
 
 
