@@ -26,6 +26,7 @@ namespace {
 constexpr int kQ = 128;     // queries per block
 constexpr int kT = 64;      // slots per tile
 constexpr int kRing = 2;    // tiles in LDS
+constexpr int kW = 64;      // queries at a time in the weights' kernel
 constexpr float kRaise = 8.0f;
 
 // The slots some query of a block sees, as tiles of kT.
@@ -417,7 +418,7 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(KvView c, KvAttnArgs a, 
     const uint32_t see = seen(at0);
     for (int k = 0; k < 32; ++k) {
       if (!((bits >> k) & 1)) continue;
-      const int t = t0 + k, pg = table[t >> c.page_shift];
+      const int t = t0 + k, pg = t < tl.n ? table[t >> c.page_shift] : -1;
       if (!c.page_ok(pg)) continue;
       const T* vp = vb + (int64_t)pg * c.page_stride + (int64_t)(t & (c.page_size - 1)) * c.dim + 4 * half;
 #pragma unroll
@@ -460,10 +461,8 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(KvView c, KvAttnArgs a, 
     for (int s = 0; s < tl.total; ++s) {
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");  // this wave's rows of tile s have landed
       const bool in_part = s < all_lo || s >= all_hi;
-      if (in_part) {
-        clean(s);
-        if (tid < 2) odd[(s + 2) & 3][tid] = 0u;  // read last by tile s - 2, written next two barriers from here
-      }
+      if (in_part) clean(s);
+      if (tid < 2) odd[(s + 2) & 3][tid] = 0u;  // read last by tile s - 2, written next two barriers from here
       lds_barrier();  // tile s is in LDS for every wave, tile s - 1 is read by none
       const uint64_t good = __ballot(c.page_ok(pg));
       const uint32_t on_page = (uint32_t)(good >> (8 * (s & 7))) & 0xffu;
@@ -543,7 +542,7 @@ __global__ __launch_bounds__(256, 2) void prompt_weights_kernel(KvView c, KvAttn
   using KT = KvType<T>;
   using x8 = typename KT::x8;
   using R = Ring<QS>;
-  constexpr int kRows = 64 / R::kLpr, kDma = 16 / kRows, kBytes = kT * R::kPitch;
+  constexpr int kRows = 64 / R::kLpr, kDma = 16 / kRows, kBytes = kW * R::kPitch;
   __shared__ __attribute__((aligned(1024))) char smem[2 * kBytes];
   const GPTQ_LDS char* lds = (const GPTQ_LDS char*)smem;
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
@@ -585,8 +584,8 @@ __global__ __launch_bounds__(256, 2) void prompt_weights_kernel(KvView c, KvAttn
     const int64_t last = (int64_t)t00 + 127 + a.window - base;  // first query that no longer sees slot t00 + 127
     if (last < i_hi) i_hi = (int)last;
   }
-  i_lo &= ~(kT - 1);
-  const int steps = i_hi > i_lo ? (i_hi - i_lo + kT - 1) / kT : 0, total = steps * group;
+  i_lo &= ~(kW - 1);
+  const int steps = i_hi > i_lo ? (i_hi - i_lo + kW - 1) / kW : 0, total = steps * group;
 
   // this wave's 16 rows of every 64 queries; rows behind the last repeat it (and are masked)
   const int lrow = lane / R::kLpr, lpos = lane % R::kLpr;
@@ -597,7 +596,7 @@ __global__ __launch_bounds__(256, 2) void prompt_weights_kernel(KvView c, KvAttn
     int hh, i;
   };
   auto after = [&](At p) __attribute__((always_inline)) {
-    return p.i + kT < i_hi ? At{p.hh, p.i + kT} : At{p.hh + 1, i_lo};
+    return p.i + kW < i_hi ? At{p.hh, p.i + kW} : At{p.hh + 1, i_lo};
   };
   auto stage = [&](int s, At p) __attribute__((always_inline)) {
     const int hh = p.hh, i0 = p.i + 16 * wave;
