@@ -372,7 +372,7 @@ typedef struct {
  *           elements apart (% 8 == 0), 16-byte aligned; not in the cache.
  *  cu_seqlens device int32 [n_seqs + 1]: sequence b's rows are cu_seqlens[b] ..
  *           cu_seqlens[b + 1] - 1, ascending from 0; rows behind the last
- *           sequence are not read. NULL: one row per sequence (n_tokens ==
+ *           sequence are ignored. NULL: one row per sequence (n_tokens ==
  *           n_seqs). A sequence may have none.
  * Slots below 0 or beyond the table are skipped. Two sequences whose new slots
  * share a page row leave one of the two there. */
@@ -392,7 +392,7 @@ size_t gptq_kv_workspace_bytes(const gptq_kv_cache_t* cache, const gptq_kv_seqs_
  * t < sinks, w_t = softmax_t(scale q_h . k_g[t]) and out_h = sum_t w_t v_g[t]. A
  * sequence that sees nothing (length 0) gives zeros.
  *  q        device [n_seqs][n_heads][head_dim], sequences ldq elements apart
- *           (% 8 == 0), 16-byte aligned.  out: the same with ldo; may be q.
+ *           (% 8 == 0, below 2^26), 16-byte aligned.  out: the same with ldo; may be q.
  *  n_heads  a multiple of n_kv_heads, at most 1024 per kv head.
  *  scale    finite (1 / sqrt(head_dim) in OPT).
  *  window   0: every slot; else the last `window` slots. sinks >= 0: first slots

@@ -6,5 +6,5 @@ names, and the seeded synthetic layer generator.
 """
 
 from . import synthetic  # noqa: F401
-from .gptq import (accumulate_hessian, load_library, pack_codes, prepare_hinv,  # noqa: F401
-                   quantize, quantize_layer, workspace_bytes)
+from .gptq import (accumulate_hessian, kv_append, kv_evict, load_library, pack_codes,  # noqa: F401
+                   paged_attention, paged_prefill, prepare_hinv, quantize, quantize_layer, workspace_bytes)

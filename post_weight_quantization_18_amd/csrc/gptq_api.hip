@@ -111,6 +111,7 @@ gptq_status_t kv_attn_args(const KvView& c, const void* q, int64_t ldq, int64_t 
   const int64_t cap = (int64_t)c.max_pages * c.page_size;
   if (!q || !out || n_heads <= 0 || n_heads % c.n_kv) return GPTQ_ERR_INVALID_ARG;
   if (n_heads / c.n_kv > 1024) return GPTQ_ERR_UNSUPPORTED;
+  if (ldq >= (1 << 26) || ldo >= (1 << 26)) return GPTQ_ERR_UNSUPPORTED;  // rows of up to 128 MB
   if (ldq % 8 || ldo % 8 || ldq < n_heads * c.dim || ldo < n_heads * c.dim) return GPTQ_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(out, 16)) return GPTQ_ERR_INVALID_ARG;
   if (!(scale - scale == 0.0f) || window < 0 || sinks < 0) return GPTQ_ERR_INVALID_ARG;

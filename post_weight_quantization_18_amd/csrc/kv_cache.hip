@@ -45,9 +45,11 @@ __global__ __launch_bounds__(256) void append_kernel(KvView c, const uint4v* k_n
   for (int t = 0; t < TOK; ++t)
     page[t] = c.table[(int64_t)(b[t] < 0 ? 0 : b[t]) * c.ld_table + ((slot[t] < 0 ? 0 : slot[t]) >> c.page_shift)];
 #pragma unroll
-  for (int t = 0; t < TOK; ++t)
+  for (int t = 0; t < TOK; ++t) {
+    GPTQ_DASSERT(b[t] < c.n_seqs && slot[t] < cap);
     if (slot[t] >= 0 && c.page_ok(page[t]))
       *(uint4v*)(dst + c.head_base(page[t], h) + (slot[t] & (c.page_size - 1)) * c.dim + off) = x[t];
+  }
 }
 
 // Order-preserving key of a sum: larger weight, larger key; a NaN above all, and

@@ -222,6 +222,7 @@ __global__ __launch_bounds__(64 * NW, 2) void token_kernel(KvView c, KvAttnArgs 
     const int t0 = st.slot0(s);
     const int pk = c.page_ok(p.k) ? p.k : 0, pv = c.page_ok(p.v) ? p.v : 0;
     const int rk = (t0 + 8 * (cl >> 2) + (cl & 3)) & (c.page_size - 1), rv = (t0 + 8 * g) & (c.page_size - 1);
+    GPTQ_DASSERT(pk >= 0 && pk < c.n_pages && pv >= 0 && pv < c.n_pages && t0 >= 0 && t0 < st.n);
     const T* kp = kbase + (int64_t)pk * c.page_stride + rk * c.dim;
     const T* vp = vbase + (int64_t)pv * c.page_stride + rv * c.dim + vch;
 #pragma unroll
@@ -422,8 +423,8 @@ __device__ __forceinline__ void join_ml(const float* ml, int n_splits, float* m,
   float mm = -INFINITY, ll = 0.0f;
   for (int s = lane; s < n_splits; s += 64) mm = fmaxf(mm, ml[2 * s]);
   for (int o = 32; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor(mm, o));
-  const float base = mm == -INFINITY ? 0.0f : mm;  // (a sum over nothing visible is 0 or, from a NaN score, NaN)
-  for (int s = lane; s < n_splits; s += 64) ll += __builtin_amdgcn_exp2f(ml[2 * s] - base) * ml[2 * s + 1] + 0.0f * ml[2 * s + 1];
+  const float base = mm == -INFINITY ? 0.0f : mm;
+  for (int s = lane; s < n_splits; s += 64) ll += __builtin_amdgcn_exp2f(ml[2 * s] - base) * ml[2 * s + 1];
   for (int o = 32; o > 0; o >>= 1) ll += __shfl_xor(ll, o);
   *m = base;
   *l = ll;

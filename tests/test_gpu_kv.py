@@ -98,6 +98,7 @@ TOKEN = [
     ("bf16", [1025], 2, 2, 128, 256, 7, 1),
     ("fp16", [2300, 700], 1, 1, 128, 64, 0, 0),        # many splits
     ("fp16", [9000], 256, 256, 8, 256, 0, 0),          # whole, scores too many for LDS
+    ("fp16", [500, 3], 32, 2, 128, 16, 0, 0),          # 16 heads a key: all the LDS that the scores may take
     ("bf16", [2100, 40, 0], 34, 2, 64, 32, 1500, 3),   # 17 heads a key, splits and a window
 ]
 

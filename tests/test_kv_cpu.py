@@ -89,6 +89,7 @@ def test_attention_refusals(lib, prompt):
     assert call(heads=0) == BAD and call(heads=3) == BAD and call(heads=-4) == BAD
     assert call(heads=4096, ldq=4096 * 64, ldo=4096 * 64) == UNSUP          # 2048 heads a key
     assert call(ldq=248) == BAD and call(ldo=260) == BAD
+    assert call(ldq=1 << 26) == UNSUP and call(ldo=1 << 26) == UNSUP
     assert call(q=P + 8) == BAD and call(out=(P << 1) + 2) == BAD
     for s in (float("nan"), float("inf"), -float("inf")):
         assert call(scale=s) == BAD
