@@ -45,47 +45,84 @@ struct Tiles {
   __device__ __forceinline__ int slot0(int s) const { return (s < sink_tiles ? s : s - sink_tiles + jump) * kT; }
 };
 
-// Block t of the ragged batch's blocks of kQ queries: its sequence and first
-// query there; sequences in order. b = -1 behind the last one.
-struct Where {
-  int b, i0, n_b, row0;  // sequence, first query in it, its queries, its first row
-  __device__ __forceinline__ Where(const int32_t* cu, int n_seqs, int t, int n_rows) {
+// Sum over the lanes up to this one (row shifts, then the rows' last lanes broadcast).
+__device__ __forceinline__ int scan64(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, true);   // row_shr 1, 2, 4, 8
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);  // row_bcast 15, 31
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);
+  return x;
+}
+
+// The ragged batch as pieces of kQ queries, and where piece t lies: of up to 64 sequences
+// (one per lane) the pieces with the highest number in their sequence, which see most, come
+// first; of more, the sequences in order, each from its end.
+struct Pieces {
+  const KvView& c;
+  const int32_t* cu;
+  int n_rows, total, most;
+  int c0, n, len, own;  // of sequence `lane`: first row, queries, slots, pieces
+  __device__ __forceinline__ void load(int s) {
+    c0 = n = len = 0;
+    if (s < c.n_seqs) {
+      len = c.len(s);
+      c0 = cu[s];
+      const int c1 = cu[s + 1];
+      // rows outside the q tensor are not there, whatever cu says
+      n = c0 >= 0 && c1 > c0 && c1 <= n_rows ? c1 - c0 : 0;
+    }
+    own = (n + kQ - 1) / kQ;
+  }
+  __device__ __forceinline__ Pieces(const KvView& c, const int32_t* cu, int n_rows) : c(c), cu(cu), n_rows(n_rows) {
     const int lane = threadIdx.x & 63;
-    b = -1;
-    int before = 0;
-    for (int base = 0; base < n_seqs; base += 64) {
-      const int s = base + lane;
-      int c0 = 0, n = 0;
-      if (s < n_seqs) {
-        c0 = cu[s];
-        const int c1 = cu[s + 1];
-        // rows outside the q tensor are not there, whatever cu says
-        n = c0 >= 0 && c1 > c0 && c1 <= n_rows ? c1 - c0 : 0;
-      }
-      int incl = (n + kQ - 1) / kQ;
-      const int own = incl;
-      for (int o = 1; o < 64; o <<= 1) {
-        const int u = __shfl_up(incl, o);
-        if (lane >= o) incl += u;
-      }
-      const int start = before + incl - own;
-      const uint64_t hit = __ballot(t >= start && t < start + own);
-      if (hit) {
-        const int l = __builtin_ctzll(hit);
-        b = base + l;
-        i0 = (t - __shfl(start, l)) * kQ;
-        n_b = __shfl(n, l);
-        row0 = __shfl(c0, l);
-        break;
-      }
-      before += __shfl(incl, 63);
+    total = 0;
+    for (int base = 0; base < c.n_seqs; base += 64) {
+      load(base + lane);
+      total += __builtin_amdgcn_readlane(scan64(own), 63);
     }
-    if (b >= 0) {
-      b = __builtin_amdgcn_readfirstlane(b);
-      i0 = __builtin_amdgcn_readfirstlane(i0);
-      n_b = __builtin_amdgcn_readfirstlane(n_b);
-      row0 = __builtin_amdgcn_readfirstlane(row0);
+    most = own;
+    for (int o = 32; o > 0; o >>= 1) most = max(most, __shfl_xor(most, o));
+  }
+  int b, i0, n_b, row0, len_b;
+  __device__ __forceinline__ void find(int t) {
+    const int lane = threadIdx.x & 63;
+    int at = 0, base = 0, piece = 0;
+    if (c.n_seqs <= 64) {
+      // the highest level with more than t pieces at or above it
+      int lo = 0, hi = most;  // holds at lo, not at hi
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__builtin_amdgcn_readlane(scan64(max(own - mid, 0)), 63) > t)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      const int above = __builtin_amdgcn_readlane(scan64(max(own - lo - 1, 0)), 63);
+      const bool in = own > lo;
+      const int rank = scan64(in ? 1 : 0) - 1;
+      at = __builtin_ctzll(__ballot(in && rank == t - above));
+      piece = lo;
+    } else {
+      int before = 0;
+      for (;; base += 64) {
+        load(base + lane);
+        const int incl = scan64(own), start = before + incl - own;
+        const uint64_t hit = __ballot(t >= start && t < start + own);
+        if (hit || base + 64 >= c.n_seqs) {
+          at = hit ? __builtin_ctzll(hit) : 0;
+          piece = __shfl(own, at) - 1 - (t - __shfl(start, at));
+          break;
+        }
+        before += __builtin_amdgcn_readlane(incl, 63);
+      }
     }
+    b = __builtin_amdgcn_readfirstlane(base + at);
+    i0 = __builtin_amdgcn_readfirstlane(piece * kQ);
+    n_b = __builtin_amdgcn_readfirstlane(__shfl(n, at));
+    row0 = __builtin_amdgcn_readfirstlane(__shfl(c0, at));
+    len_b = __builtin_amdgcn_readfirstlane(__shfl(len, at));
   }
 };
 
@@ -180,7 +217,7 @@ struct Ring {
 // log2 of the sum of 2^score goes to lse [n_tokens][n_heads].
 template <typename T, int QS, bool LSE>
 __global__ __launch_bounds__(256, 2) void prompt_kernel(KvView c, KvAttnArgs a, const int32_t* cu, int n_rows,
-                                                        int n_blk, float* lse) {
+                                                        float* lse) {
   using KT = KvType<T>;
   using x8 = typename KT::x8;
   using R = Ring<QS>;
@@ -191,15 +228,22 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(KvView c, KvAttnArgs a, 
   __shared__ uint32_t odd[4][2];  // by tile modulo 4, a bit per slot: its values hold an infinity or NaN
   const GPTQ_LDS char* lds = (const GPTQ_LDS char*)smem;
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
-  const int id = xcd_logical_block(blockIdx.x, gridDim.x);
-  const int h = id / n_blk;
-  const Where at(cu, c.n_seqs, n_blk - 1 - (id - h * n_blk), n_rows);  // late queries see most: first
-  if (at.b < 0) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
   const int col = lane & 31, half = lane >> 5;
+  Pieces at(c, cu, n_rows);
+  // All heads' pieces, head by head, in eight parts, one for each XCD (neighbours in a head
+  // share its L2); the blocks that are too many come last.
+  const int real = at.total * a.n_heads, xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
+  if (slot >= real / 8 + (xcd < real % 8 ? 1 : 0)) return;
+  const int item = xcd * (real / 8) + min(xcd, real % 8) + slot;
+  const int h = uni(item / at.total);
+  at.find(item - h * at.total);
+  const bool exact = c.dim == 16 * QS;
   const int kvh = h / (a.n_heads / c.n_kv);
-  const int len = uni(c.len(at.b));
-  const int p0 = len - at.n_b + at.i0;                         // position of the block's first query
+  // (opaque, as a per-lane value: as a scalar the compiler unrolls what hangs on it into more
+  // registers than there are)
+  int p0 = at.len_b - at.n_b + at.i0;                          // position of the block's first query
+  asm volatile("" : "+v"(p0));
   const int rows = at.n_b - at.i0 < kQ ? at.n_b - at.i0 : kQ;  // its queries
   const int first = a.window > 0 && p0 - a.window + 1 > 0 ? p0 - a.window + 1 : 0;
   const int end = p0 + rows > 0 ? p0 + rows : 0;
@@ -263,8 +307,7 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(KvView c, KvAttnArgs a, 
     off_v[i] = ((kRows * i + lrow) * c.dim + (ch < chunks ? ch : 0) * 8) * 2;
   }
   // dim = 16 QS: no product reads a chunk behind the head's end, and what lands there is not
-  // looked at. Otherwise these chunks stay as they are cleared below.
-  const bool exact = c.dim == 16 * QS;
+  // looked at. Otherwise these chunks stay cleared.
   const T* kb = (const T*)c.k + (int64_t)kvh * c.page_size * c.dim;
   const T* vb = (const T*)c.v + (int64_t)kvh * c.page_size * c.dim;
   // pages of the octets of eight tiles, one per lane
@@ -284,8 +327,9 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(KvView c, KvAttnArgs a, 
         if (exact) {
           dma16_octet<kDma>(kb + from, vb + from, off_k[oc], off_v, to_oc, to_oc + R::kHalf);
         } else {
-          int lp = lpos;
+          int lp = lpos, chunks = c.dim >> 3;
           asm volatile("" : "+v"(lp));
+          asm volatile("" : "+s"(chunks));
 #pragma unroll
           for (int i = 0; i < kDma; ++i) {
             if ((lp ^ R::fk(8 * oc + kRows * i + lrow)) < chunks) dma16_from(kb + from, off_k[oc][i], to_oc + 1024 * i);
@@ -413,8 +457,9 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(KvView c, KvAttnArgs a, 
   // rare: values of a tile that are not finite, for the queries that see them (their weight is
   // positive, so the sum is what the value is)
   auto add_odd = [&](int t0, uint32_t bits) __attribute__((always_inline)) {
-    int at0 = t0;
+    int at0 = t0, dim = c.dim;
     asm volatile("" : "+v"(at0));
+    asm volatile("" : "+s"(dim));
     const uint32_t see = seen(at0);
     for (int k = 0; k < 32; ++k) {
       if (!((bits >> k) & 1)) continue;
@@ -427,7 +472,7 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(KvView c, KvAttnArgs a, 
         for (int r4 = 0; r4 < 4; ++r4) {
           typedef T x4 __attribute__((ext_vector_type(4)));
           x4 z = (x4){0, 0, 0, 0};
-          if (32 * i + 8 * r4 < c.dim) z = *(const x4*)(vp + 32 * i + 8 * r4);
+          if (32 * i + 8 * r4 < dim) z = *(const x4*)(vp + 32 * i + 8 * r4);
 #pragma unroll
           for (int r = 0; r < 4; ++r)
             o[i][4 * r4 + r] += ((see >> k) & 1) && !(__builtin_fabsf((float)z[r]) < INFINITY) ? (float)z[r] : 0.0f;
@@ -438,6 +483,9 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(KvView c, KvAttnArgs a, 
 
   if (tl.total > 0) {
     if (tid < 8) odd[tid >> 1][tid & 1] = 0u;
+    if (!exact)
+      for (int i = tid; i < R::kBytes / 16; i += 256) *(GPTQ_LDS uint4v*)(lds + 16 * i) = (uint4v){0, 0, 0, 0};
+    // elements between the head's end and the row's are never transferred: zeros once and for all
     if (!exact)
       for (int i = tid; i < R::kBytes / 16; i += 256) *(GPTQ_LDS uint4v*)(lds + 16 * i) = (uint4v){0, 0, 0, 0};
     int pg = pages(0), pg_next = pages(1);
@@ -505,27 +553,30 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(KvView c, KvAttnArgs a, 
   }
 
   lsum += __shfl_xor(lsum, 32);
-  if (qi >= rows) return;
-  const float inv = lsum == 0.0f ? 0.0f : 1.0f / lsum;
-  const int64_t row = at.row0 + at.i0 + qi;
-  T* op = (T*)a.out + row * a.ldo + (int64_t)h * c.dim;
+  if (qi < rows) {
+    int dim = c.dim;
+    asm volatile("" : "+s"(dim));  // (or sixteen comparisons with it are kept from piece to piece)
+    const float inv = lsum == 0.0f ? 0.0f : 1.0f / lsum;
+    const int64_t row = at.row0 + at.i0 + qi;
+    T* op = (T*)a.out + row * a.ldo + (int64_t)h * c.dim;
 #pragma unroll
-  for (int i = 0; i < NO; ++i)
+    for (int i = 0; i < NO; ++i)
 #pragma unroll
-    for (int r4 = 0; r4 < 4; ++r4) {
-      const int e = 32 * i + 8 * r4 + 4 * half;
-      if (e < c.dim) {
-        typedef T x4 __attribute__((ext_vector_type(4)));
-        x4 z;
+      for (int r4 = 0; r4 < 4; ++r4) {
+        const int e = 32 * i + 8 * r4 + 4 * half;
+        if (e < dim) {
+          typedef T x4 __attribute__((ext_vector_type(4)));
+          x4 z;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) z[r] = lsum == 0.0f ? (T)0.0f : (T)(o[i][4 * r4 + r] * inv);
-        *(x4*)(op + e) = z;
+          for (int r = 0; r < 4; ++r) z[r] = lsum == 0.0f ? (T)0.0f : (T)(o[i][4 * r4 + r] * inv);
+          *(x4*)(op + e) = z;
+        }
       }
+    if constexpr (LSE) {
+      // a row without a weight: +infinity, so that 2^(score - lse) is 0
+      if (half == 0)
+        lse[row * a.n_heads + h] = lsum == 0.0f ? INFINITY : (m == -INFINITY ? 0.0f : m * sc) + log2f(lsum);
     }
-  if constexpr (LSE) {
-    // a row without a weight: +infinity, so that 2^(score - lse) is 0
-    if (half == 0)
-      lse[row * a.n_heads + h] = lsum == 0.0f ? INFINITY : (m == -INFINITY ? 0.0f : m * sc) + log2f(lsum);
   }
 }
 
@@ -679,11 +730,12 @@ __global__ __launch_bounds__(256, 2) void prompt_weights_kernel(KvView c, KvAttn
 template <typename T, int QS, bool LSE>
 gptq_status_t launch_rows(const KvView& c, const KvAttnArgs& a, const int32_t* cu, int64_t n_tokens, float* lse,
                           hipStream_t st) {
-  const int64_t n_blk = n_tokens / kQ + c.n_seqs;  // at least the ragged batch's blocks
-  const int64_t blocks = n_blk * a.n_heads;
+  // at least the ragged batch's pieces; blocks in eights, one for each XCD
+  const int64_t pieces = (n_tokens / kQ + c.n_seqs) * a.n_heads;
+  const int64_t blocks = ceil_div(pieces, 8) * 8;
   if (blocks * 256 >= (int64_t)1 << 32) return GPTQ_ERR_UNSUPPORTED;
   hipLaunchKernelGGL((prompt_kernel<T, QS, LSE>), dim3((unsigned)blocks), dim3(256), Ring<QS>::kBytes, st, c, a, cu,
-                     (int)n_tokens, (int)n_blk, lse);
+                     (int)n_tokens, lse);
   GPTQ_CHECK_LAUNCH();
   return GPTQ_OK;
 }
