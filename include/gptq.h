@@ -421,7 +421,11 @@ gptq_status_t gptq_paged_attention(const gptq_kv_cache_t* cache, const gptq_kv_s
  *  cu_seqlens device int32 [n_seqs + 1], ascending from 0; a sequence whose
  *           bounds leave [0, n_tokens] is passed over. n_tokens < 2^30.
  *  weights  += the sum of w_t over the sequence's rows and the heads of a group.
- * The weights enter the second product in the cache's type. */
+ *  workspace as above, for n_tokens rows (few rows over many slots need one for
+ *           partial results, and any call with weights).
+ * The weights enter the second product in the cache's type. The order of the sums
+ * depends on the sizes given from the host (n_tokens, n_seqs, max_pages), not on
+ * lens or timing. */
 gptq_status_t gptq_paged_prefill(const gptq_kv_cache_t* cache, const gptq_kv_seqs_t* seqs, const void* q, int64_t ldq,
                                  const int32_t* cu_seqlens, int64_t n_tokens, int64_t n_heads, float scale,
                                  int64_t window, int64_t sinks, float* weights, int64_t ldw, void* out, int64_t ldo,

@@ -332,7 +332,7 @@ size_t gptq_kv_workspace_bytes(const gptq_kv_cache_t* cache, const gptq_kv_seqs_
   KvView c;
   if (kv_view(cache, seqs, &c) || n_heads <= 0 || n_heads % c.n_kv || n_heads / c.n_kv > 1024) return 0;
   if (window < 0 || sinks < 0 || n_tokens < 0 || n_tokens >= ((int64_t)1 << 30)) return 0;
-  if (n_tokens > 0) return kv_prompt_workspace_bytes(n_tokens, n_heads, weights != 0);
+  if (n_tokens > 0) return kv_prompt_workspace_bytes(c, n_tokens, n_heads, window, sinks, weights != 0);
   return kv_token_workspace_bytes(c, n_heads, window, sinks, weights != 0);
 }
 
@@ -363,7 +363,7 @@ gptq_status_t gptq_paged_prefill(const gptq_kv_cache_t* cache, const gptq_kv_seq
   if (const gptq_status_t s = kv_attn_args(c, q, ldq, n_heads, scale, window, sinks, weights, ldw, out, ldo, &a))
     return s;
   if (out == q) return GPTQ_ERR_INVALID_ARG;
-  const size_t need = kv_prompt_workspace_bytes(n_tokens, n_heads, weights != nullptr);
+  const size_t need = kv_prompt_workspace_bytes(c, n_tokens, n_heads, a.window, a.sinks, weights != nullptr);
   if (need && (!workspace || ws_bytes < need || !aligned(workspace, 256))) return GPTQ_ERR_WORKSPACE;
   GPTQ_CHECK_DEVICE();
   return kv_prompt_enqueue(c, a, cu_seqlens, n_tokens, workspace, (hipStream_t)stream);

@@ -95,7 +95,20 @@ struct KvAttnArgs {
 size_t kv_token_workspace_bytes(const KvView& c, int64_t n_heads, int64_t window, int64_t sinks, bool weights);
 gptq_status_t kv_token_enqueue(const KvView& c, const KvAttnArgs& a, void* ws, hipStream_t st);
 
-size_t kv_prompt_workspace_bytes(int64_t n_tokens, int64_t n_heads, bool weights);
+// Partial results of rows whose slots are split over blocks: per (row, head, split) the
+// running maximum (in powers of two) and the sum, and the unnormalized output.
+struct SplitWs {
+  float* ml;  // [rows * n_heads][n_splits][2]
+  float* o;   // [rows * n_heads][n_splits][dim]
+  int n_splits;
+};
+// Joins them into those of the n_rows rows of out that a sequence of the ragged batch cu has;
+// lse (optional): log2 of the sum of 2^score per row and head.
+gptq_status_t kv_join_enqueue(const KvView& c, const KvAttnArgs& a, const SplitWs& w, int64_t n_rows,
+                              const int32_t* cu, float* lse, hipStream_t st);
+
+size_t kv_prompt_workspace_bytes(const KvView& c, int64_t n_tokens, int64_t n_heads, int64_t window, int64_t sinks,
+                                 bool weights);
 gptq_status_t kv_prompt_enqueue(const KvView& c, const KvAttnArgs& a, const int32_t* cu, int64_t n_tokens, void* ws,
                                 hipStream_t st);
 

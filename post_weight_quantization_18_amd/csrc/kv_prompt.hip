@@ -18,6 +18,8 @@
 // that the operand reads meet no bank twice. V's operand needs 8 slots of one
 // element per lane: transpose reads give it. Two blocks share a compute unit:
 // the matrix products of one run beside the softmax of the other.
+#include <algorithm>
+
 #include "kv.h"
 
 namespace gptq {
@@ -26,6 +28,7 @@ namespace {
 constexpr int kQ = 128;     // queries per block
 constexpr int kT = 64;      // slots per tile
 constexpr int kRing = 2;    // tiles in LDS
+constexpr int kLeast = 4;   // tiles per block where they are split
 constexpr int kW = 64;      // queries at a time in the weights' kernel
 constexpr float kRaise = 8.0f;
 
@@ -82,6 +85,7 @@ struct Pieces {
       load(base + lane);
       total += __builtin_amdgcn_readlane(scan64(own), 63);
     }
+    total = min(total, n_rows / kQ + c.n_seqs);  // (more only if cu is not ascending)
     most = own;
     for (int o = 32; o > 0; o >>= 1) most = max(most, __shfl_xor(most, o));
   }
@@ -213,11 +217,15 @@ struct Ring {
   static constexpr __device__ int fv(int r) { return QS <= 4 ? 4 * ((r >> 1) & 1) : 4 * (r & 3); }
 };
 
-// QS: steps of 16 along the head for the scores (16 QS >= dim). LSE: the row's
-// log2 of the sum of 2^score goes to lse [n_tokens][n_heads].
-template <typename T, int QS, bool LSE>
+// What a block leaves: its rows of out; with them the rows' log2 of the sum of 2^score in
+// lse [n_tokens][n_heads]; or, where a piece's tiles are split over n_splits blocks, the
+// unnormalized sums with their maximum and weight in parts [n_tokens][n_heads][n_splits].
+constexpr int kOut = 0, kOutLse = 1, kParts = 2;
+
+// QS: steps of 16 along the head for the scores (16 QS >= dim).
+template <typename T, int QS, int MODE>
 __global__ __launch_bounds__(256, 2) void prompt_kernel(KvView c, KvAttnArgs a, const int32_t* cu, int n_rows,
-                                                        float* lse) {
+                                                        float* lse, SplitWs parts) {
   using KT = KvType<T>;
   using x8 = typename KT::x8;
   using R = Ring<QS>;
@@ -233,9 +241,12 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(KvView c, KvAttnArgs a, 
   Pieces at(c, cu, n_rows);
   // All heads' pieces, head by head, in eight parts, one for each XCD (neighbours in a head
   // share its L2); the blocks that are too many come last.
-  const int real = at.total * a.n_heads, xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
+  const int n_splits = MODE == kParts ? parts.n_splits : 1;
+  const int real = at.total * a.n_heads * n_splits, xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
   if (slot >= real / 8 + (xcd < real % 8 ? 1 : 0)) return;
-  const int item = xcd * (real / 8) + min(xcd, real % 8) + slot;
+  int item = xcd * (real / 8) + min(xcd, real % 8) + slot;
+  const int split = MODE == kParts ? item % n_splits : 0;
+  if constexpr (MODE == kParts) item /= n_splits;
   const int h = uni(item / at.total);
   at.find(item - h * at.total);
   const bool exact = c.dim == 16 * QS;
@@ -481,16 +492,17 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(KvView c, KvAttnArgs a, 
     }
   };
 
-  if (tl.total > 0) {
+  // this block's tiles
+  const int per = MODE == kParts ? max(kLeast, (tl.total + n_splits - 1) / n_splits) : tl.total;
+  const int s0 = uni(split * per), s1 = uni(min(s0 + per, tl.total));
+  if (s0 < s1) {
     if (tid < 8) odd[tid >> 1][tid & 1] = 0u;
-    if (!exact)
-      for (int i = tid; i < R::kBytes / 16; i += 256) *(GPTQ_LDS uint4v*)(lds + 16 * i) = (uint4v){0, 0, 0, 0};
     // elements between the head's end and the row's are never transferred: zeros once and for all
     if (!exact)
       for (int i = tid; i < R::kBytes / 16; i += 256) *(GPTQ_LDS uint4v*)(lds + 16 * i) = (uint4v){0, 0, 0, 0};
-    int pg = pages(0), pg_next = pages(1);
+    int pg = pages(s0 >> 3), pg_next = pages((s0 >> 3) + 1);
     __syncthreads();
-    stage(0, pg);
+    stage(s0, pg);
     // raises the running maximum to those of x and y if a score is far above it
     auto raise_to = [&](const float16v& x, const float16v& y) __attribute__((always_inline)) {
       float top = fmaxf(x[0], y[0]);
@@ -506,7 +518,7 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(KvView c, KvAttnArgs a, 
       }
       return m == -INFINITY ? 0.0f : m * sc;
     };
-    for (int s = 0; s < tl.total; ++s) {
+    for (int s = s0; s < s1; ++s) {
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");  // this wave's rows of tile s have landed
       const bool in_part = s < all_lo || s >= all_hi;
       if (in_part) clean(s);
@@ -518,7 +530,7 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(KvView c, KvAttnArgs a, 
         pg = pg_next;
         pg_next = pages((s >> 3) + 2);
       }
-      if (s + 1 < tl.total) stage(s + 1, pg);
+      if (s + 1 < s1) stage(s + 1, pg);
       const GPTQ_LDS char* b = lds + (s & 1) * R::kTileBytes;
       x8 px[2], py[2];
       if (!in_part && on_page == 0xffu) {
@@ -558,6 +570,23 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(KvView c, KvAttnArgs a, 
     asm volatile("" : "+s"(dim));  // (or sixteen comparisons with it are kept from piece to piece)
     const float inv = lsum == 0.0f ? 0.0f : 1.0f / lsum;
     const int64_t row = at.row0 + at.i0 + qi;
+    if constexpr (MODE == kParts) {
+      const int64_t part = (row * a.n_heads + h) * n_splits + split;
+      float* pp = parts.o + part * dim;
+      // (a maximum of -infinity says that the sums are not there)
+#pragma unroll
+      for (int i = 0; i < NO; ++i)
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4) {
+          const int e = 32 * i + 8 * r4 + 4 * half;
+          if (s0 < s1 && e < dim) *(float4v*)(pp + e) = (float4v){o[i][4 * r4], o[i][4 * r4 + 1], o[i][4 * r4 + 2], o[i][4 * r4 + 3]};
+        }
+      if (half == 0) {
+        parts.ml[2 * part] = m == -INFINITY ? -INFINITY : m * sc;
+        parts.ml[2 * part + 1] = lsum;
+      }
+      return;
+    }
     T* op = (T*)a.out + row * a.ldo + (int64_t)h * c.dim;
 #pragma unroll
     for (int i = 0; i < NO; ++i)
@@ -572,7 +601,7 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(KvView c, KvAttnArgs a, 
           *(x4*)(op + e) = z;
         }
       }
-    if constexpr (LSE) {
+    if constexpr (MODE == kOutLse) {
       // a row without a weight: +infinity, so that 2^(score - lse) is 0
       if (half == 0)
         lse[row * a.n_heads + h] = lsum == 0.0f ? INFINITY : (m == -INFINITY ? 0.0f : m * sc) + log2f(lsum);
@@ -727,27 +756,79 @@ __global__ __launch_bounds__(256, 2) void prompt_weights_kernel(KvView c, KvAttn
   }
 }
 
-template <typename T, int QS, bool LSE>
+int64_t pieces_of(const KvView& c, int64_t n_tokens, int64_t n_heads) {
+  return (n_tokens / kQ + c.n_seqs) * n_heads;
+}
+
+// Blocks per piece. Few queries over a long cache are few pieces with many tiles: they are
+// split until there are two blocks for each compute unit, at least kLeast tiles each (512
+// queries, 8 heads of 128, 8512 slots: 184 us whole, 41 split; 128 queries, 32 heads, 30128
+// slots: 637 and 95). A tile takes 1.3 us, with two blocks on a compute unit half as much again;
+// partial results and their join cost three tiles' time, and one more per 7000 rows of them.
+// Where that is more than what splitting saves, pieces stay whole (512 queries, 64 heads, 1012
+// slots: 31 us whole, 38 split; 8512 slots: 184 and 165).
+int64_t splits_of(const KvView& c, int64_t n_tokens, int64_t n_heads, int64_t window, int64_t sinks) {
+  const int64_t cap = (int64_t)c.max_pages << c.page_shift, all = ceil_div(cap, kT);
+  int64_t tiles = all;
+  if (window > 0 && window < cap)
+    tiles = std::min(all, ceil_div(std::min(sinks, cap), kT) + (window + kQ) / kT + 2);
+  const int64_t pieces = c.n_seqs * ceil_div(ceil_div(n_tokens, c.n_seqs), kQ) * n_heads;  // were all of one length
+  const int64_t s = std::min(512 / pieces, tiles / kLeast);
+  if (s <= 1) return 1;
+  const int64_t saved = tiles * (2 * s - (pieces * s > 256 ? 3 : 2)) / (2 * s);
+  return saved < 3 + n_tokens * n_heads * s / 7000 ? 1 : s;
+}
+
+struct PromptWs {
+  float* lse;
+  SplitWs parts;
+};
+PromptWs layout(const KvView& c, int64_t n_tokens, int64_t n_heads, int64_t window, int64_t sinks, bool weights,
+                void* ws, size_t* bytes) {
+  PromptWs w{};
+  const int64_t rows = n_tokens * n_heads;
+  float* f = (float*)ws;
+  size_t n = 0;
+  w.parts.n_splits = (int)splits_of(c, n_tokens, n_heads, window, sinks);
+  if (w.parts.n_splits > 1) {
+    w.parts.o = f + n;
+    n += (size_t)rows * w.parts.n_splits * c.dim;
+    w.parts.ml = f + n;
+    n += (size_t)rows * w.parts.n_splits * 2;
+  }
+  w.lse = f + n;
+  if (weights) n += (size_t)rows;
+  if (bytes) *bytes = n * sizeof(float);
+  return w;
+}
+
+template <typename T, int QS, int MODE>
 gptq_status_t launch_rows(const KvView& c, const KvAttnArgs& a, const int32_t* cu, int64_t n_tokens, float* lse,
-                          hipStream_t st) {
+                          const SplitWs& parts, hipStream_t st) {
   // at least the ragged batch's pieces; blocks in eights, one for each XCD
-  const int64_t pieces = (n_tokens / kQ + c.n_seqs) * a.n_heads;
-  const int64_t blocks = ceil_div(pieces, 8) * 8;
+  const int64_t blocks = ceil_div(pieces_of(c, n_tokens, a.n_heads) * parts.n_splits, 8) * 8;
   if (blocks * 256 >= (int64_t)1 << 32) return GPTQ_ERR_UNSUPPORTED;
-  hipLaunchKernelGGL((prompt_kernel<T, QS, LSE>), dim3((unsigned)blocks), dim3(256), Ring<QS>::kBytes, st, c, a, cu,
-                     (int)n_tokens, lse);
+  hipLaunchKernelGGL((prompt_kernel<T, QS, MODE>), dim3((unsigned)blocks), dim3(256), Ring<QS>::kBytes, st, c, a, cu,
+                     (int)n_tokens, lse, parts);
   GPTQ_CHECK_LAUNCH();
   return GPTQ_OK;
 }
 
 template <typename T, int QS>
-gptq_status_t launch(const KvView& c, const KvAttnArgs& a, const int32_t* cu, int64_t n_tokens, float* lse,
+gptq_status_t launch(const KvView& c, const KvAttnArgs& a, const int32_t* cu, int64_t n_tokens, const PromptWs& w,
                      hipStream_t st) {
   const int64_t cap = (int64_t)c.max_pages << c.page_shift, n_tiles = ceil_div(cap, 128);
   const int64_t wblocks = n_tiles * c.n_kv * c.n_seqs;
   if (wblocks * 256 >= (int64_t)1 << 32) return GPTQ_ERR_UNSUPPORTED;
-  const gptq_status_t rc = a.weights ? launch_rows<T, QS, true>(c, a, cu, n_tokens, lse, st)
-                                     : launch_rows<T, QS, false>(c, a, cu, n_tokens, lse, st);
+  float* lse = w.lse;
+  gptq_status_t rc;
+  if (w.parts.n_splits > 1) {
+    rc = launch_rows<T, QS, kParts>(c, a, cu, n_tokens, lse, w.parts, st);
+    if (rc == GPTQ_OK) rc = kv_join_enqueue(c, a, w.parts, n_tokens, cu, a.weights ? lse : nullptr, st);
+  } else {
+    rc = a.weights ? launch_rows<T, QS, kOutLse>(c, a, cu, n_tokens, lse, w.parts, st)
+                   : launch_rows<T, QS, kOut>(c, a, cu, n_tokens, lse, w.parts, st);
+  }
   if (rc != GPTQ_OK || !a.weights) return rc;
   hipLaunchKernelGGL((prompt_weights_kernel<T, QS>), dim3((unsigned)wblocks), dim3(256), 0, st, c, a, cu,
                      (int)n_tokens, lse);
@@ -757,25 +838,28 @@ gptq_status_t launch(const KvView& c, const KvAttnArgs& a, const int32_t* cu, in
 
 // Steps along the head: 5 is OPT-2.7B's head of 80, which 6 would slow by a sixth.
 template <typename T>
-gptq_status_t prompt_enqueue(const KvView& c, const KvAttnArgs& a, const int32_t* cu, int64_t n_tokens, float* lse,
-                             hipStream_t st) {
-  if (c.dim <= 64) return launch<T, 4>(c, a, cu, n_tokens, lse, st);
-  if (c.dim <= 80) return launch<T, 5>(c, a, cu, n_tokens, lse, st);
-  if (c.dim <= 96) return launch<T, 6>(c, a, cu, n_tokens, lse, st);
-  return launch<T, 8>(c, a, cu, n_tokens, lse, st);
+gptq_status_t prompt_enqueue(const KvView& c, const KvAttnArgs& a, const int32_t* cu, int64_t n_tokens,
+                             const PromptWs& w, hipStream_t st) {
+  if (c.dim <= 64) return launch<T, 4>(c, a, cu, n_tokens, w, st);
+  if (c.dim <= 80) return launch<T, 5>(c, a, cu, n_tokens, w, st);
+  if (c.dim <= 96) return launch<T, 6>(c, a, cu, n_tokens, w, st);
+  return launch<T, 8>(c, a, cu, n_tokens, w, st);
 }
 
 }  // namespace
 
-size_t kv_prompt_workspace_bytes(int64_t n_tokens, int64_t n_heads, bool weights) {
-  return weights ? (size_t)n_tokens * n_heads * sizeof(float) : 0;
+size_t kv_prompt_workspace_bytes(const KvView& c, int64_t n_tokens, int64_t n_heads, int64_t window, int64_t sinks,
+                                 bool weights) {
+  size_t bytes = 0;
+  layout(c, n_tokens, n_heads, window, sinks, weights, nullptr, &bytes);
+  return bytes;
 }
 
 gptq_status_t kv_prompt_enqueue(const KvView& c, const KvAttnArgs& a, const int32_t* cu, int64_t n_tokens, void* ws,
                                 hipStream_t st) {
   TraceScope tr(st, GPTQ_TRACE_KV_ATTENTION);
-  return c.bf16 ? prompt_enqueue<bf16_t>(c, a, cu, n_tokens, (float*)ws, st)
-                : prompt_enqueue<half_t>(c, a, cu, n_tokens, (float*)ws, st);
+  const PromptWs w = layout(c, n_tokens, a.n_heads, a.window, a.sinks, a.weights != nullptr, ws, nullptr);
+  return c.bf16 ? prompt_enqueue<bf16_t>(c, a, cu, n_tokens, w, st) : prompt_enqueue<half_t>(c, a, cu, n_tokens, w, st);
 }
 
 }  // namespace gptq

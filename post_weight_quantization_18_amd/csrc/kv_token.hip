@@ -69,13 +69,11 @@ __device__ __forceinline__ int longest(const KvView& c, int i) {
   return __builtin_ctzll(__ballot(rank == i && lane < c.n_seqs));
 }
 
-// Elements of the workspace (floats): per (sequence, head, split) the running
-// maximum, the sum and the unnormalized output; then the scores by step.
+// The workspace: the splits' partial results (rows are sequences), then the scores by step.
 struct TokenWs {
-  float* ml;      // [n_seqs * n_heads][n_splits][2]
-  float* o;       // [n_seqs * n_heads][n_splits][dim]
+  SplitWs parts;
   float* scores;  // [n_seqs * n_heads][n_scores]
-  int n_splits, n_scores;
+  int n_scores;
   bool join;  // a second kernel
   bool lds;   // scores in LDS
 };
@@ -158,8 +156,8 @@ constexpr int kScoresGlobal = 1, kScoresLds = 2;
 constexpr size_t kScoresLdsBytes = 32 << 10;
 
 // KS: steps of 32 along the head for the scores; VEC: output elements per lane
-// (16 VEC >= dim). SPLIT: partial results to the workspace. SCORES: the
-// stored too.
+// (16 VEC >= dim). SPLIT: partial results to the workspace. SCORES: they
+// are kept too.
 template <typename T, int KS, int VEC, bool SPLIT, int SCORES>
 __global__ __launch_bounds__(64 * NW, 2) void token_kernel(KvView c, KvAttnArgs a, TokenWs w) {
   using KT = KvType<T>;
@@ -168,8 +166,8 @@ __global__ __launch_bounds__(64 * NW, 2) void token_kernel(KvView c, KvAttnArgs 
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int group = a.n_heads / c.n_kv, qt = (group + 15) / 16;  // heads in tiles of 16
   int id = blockIdx.x;
-  const int split = id % w.n_splits;
-  id /= w.n_splits;
+  const int split = id % w.parts.n_splits;
+  id /= w.parts.n_splits;
   const int h0 = (id % qt) * 16;
   id /= qt;
   const int kvh = id % c.n_kv, b = longest(c, id / c.n_kv);
@@ -180,7 +178,7 @@ __global__ __launch_bounds__(64 * NW, 2) void token_kernel(KvView c, KvAttnArgs 
   GPTQ_LDS float* lds_scores = (GPTQ_LDS float*)so + NW * n_h * kPitch;
 
   const Steps st(c.len(b), a.window, a.sinks);
-  const int per = (st.total + w.n_splits - 1) / w.n_splits;
+  const int per = (st.total + w.parts.n_splits - 1) / w.parts.n_splits;
   const int s_end = (split + 1) * per < st.total ? (split + 1) * per : st.total;
   const int32_t* table = c.table + (int64_t)b * c.ld_table;
   const int chunks = c.dim >> 3;
@@ -397,10 +395,11 @@ __global__ __launch_bounds__(64 * NW, 2) void token_kernel(KvView c, KvAttnArgs 
     }
     const int64_t bh = (int64_t)b * a.n_heads + kvh * group + h0 + hh;
     if constexpr (SPLIT) {
-      w.o[(bh * w.n_splits + split) * c.dim + e] = v;
+      const int64_t part = bh * w.parts.n_splits + split;
+      w.parts.o[part * c.dim + e] = v;
       if (e == 0) {
-        w.ml[(bh * w.n_splits + split) * 2] = mm;
-        w.ml[(bh * w.n_splits + split) * 2 + 1] = l;
+        w.parts.ml[2 * part] = mm;
+        w.parts.ml[2 * part + 1] = l;
       }
     } else {
       ((T*)a.out)[(int64_t)b * a.ldo + (int64_t)(kvh * group + h0 + hh) * c.dim + e] = (T)(l == 0.0f ? 0.0f : v / l);
@@ -430,9 +429,101 @@ __device__ __forceinline__ void join_ml(const float* ml, int n_splits, float* m,
   *l = ll;
 }
 
-// Joins the splits: the first n_seqs n_heads blocks one head's output each (8
-// groups of threads take every eighth split, 4 elements a thread), the others the
-// weights of kJoinSteps steps of one key head.
+// Joins the splits of one row and head, one per block: 8 groups of threads take every eighth
+// split, 4 elements a thread.
+template <typename T>
+__device__ __forceinline__ void join_row(const KvView& c, const KvAttnArgs& a, const SplitWs& w, int64_t bh, float* lse,
+                                         float* sh) {
+  const int tid = threadIdx.x;
+  const float* ml = w.ml + bh * w.n_splits * 2;
+  float m, l;
+  join_ml(ml, w.n_splits, &m, &l);
+  const int g = tid >> 5, e = (tid & 31) * 4;
+  const bool in = e < c.dim;
+  const float* o = w.o + bh * w.n_splits * c.dim + (in ? e : 0);
+  float4v v = {0, 0, 0, 0};
+#pragma unroll 4
+  for (int s = g; s < w.n_splits; s += 8)
+    if (ml[2 * s] != -INFINITY)
+      v += __builtin_amdgcn_exp2f(ml[2 * s] - m) * *(const float4v*)(o + (int64_t)s * c.dim);
+  *(float4v*)(sh + 4 * tid) = v;
+  __syncthreads();
+  if (g == 0 && in) {
+#pragma unroll
+    for (int k = 1; k < 8; ++k) v += *(const float4v*)(sh + 4 * (tid + 32 * k));
+    const int64_t row = bh / a.n_heads, h = bh - row * a.n_heads;
+    typedef T x4 __attribute__((ext_vector_type(4)));
+    x4 y;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) y[k] = (T)(l == 0.0f ? 0.0f : v[k] / l);
+    *(x4*)((T*)a.out + row * a.ldo + h * c.dim + e) = y;
+  }
+  if (lse && tid == 0) lse[bh] = l == 0.0f ? INFINITY : m + log2f(l);
+}
+
+// Row and head bh belong to a sequence of the ragged batch (rows behind the last one, say, stay
+// as they were): each of n threads looks at its share of the sequences.
+__device__ __forceinline__ bool owned(const KvView& c, const int32_t* cu, int n_rows, int row, int i, int n) {
+  bool any = false;
+  for (int s = i; s < c.n_seqs; s += n) {
+    const int c0 = cu[s], c1 = cu[s + 1];
+    any |= c0 >= 0 && c0 <= row && row < c1 && c1 <= n_rows;
+  }
+  return any;
+}
+
+// Joins the splits of all rows of a ragged batch, bound by reading them: many splits of few rows
+// with a block for each row and head; of up to 16 each thread of half a wave goes through all
+// (512 rows of 32 heads, 3 splits: a block each takes 25 us with the attention's 29, half a
+// wave 10).
+constexpr int kJoinFew = 16;
+
+template <typename T, bool FEW>
+__global__ __launch_bounds__(256) void join_rows_kernel(KvView c, KvAttnArgs a, SplitWs w, const int32_t* cu,
+                                                        int n_rows, float* lse) {
+  if constexpr (!FEW) {
+    __shared__ float sh[1024];
+    if (__syncthreads_or(owned(c, cu, n_rows, blockIdx.x / a.n_heads, threadIdx.x, 256)))
+      join_row<T>(c, a, w, blockIdx.x, lse, sh);
+  } else {
+    const int64_t bh = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, row = (int)(bh / a.n_heads), n = w.n_splits;
+    const uint64_t hit = __ballot(row < n_rows && owned(c, cu, n_rows, row, lane, 32));
+    if ((uint32_t)(hit >> (threadIdx.x & 32)) == 0) return;
+    const float* ml = w.ml + bh * n * 2;
+    const int mine = lane & (kJoinFew - 1);
+    const float ms = mine < n ? ml[2 * mine] : -INFINITY, ls = mine < n ? ml[2 * mine + 1] : 0.0f;
+    float m = ms;
+#pragma unroll
+    for (int o = kJoinFew / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+    if (m == -INFINITY) m = 0.0f;
+    const float f = __builtin_amdgcn_exp2f(ms - m);
+    float l = f * ls;
+#pragma unroll
+    for (int o = kJoinFew / 2; o > 0; o >>= 1) l += __shfl_xor(l, o);
+    const int e = 4 * lane;
+    const bool in = e < c.dim;
+    const float* op = w.o + bh * n * c.dim + (in ? e : 0);
+    float4v v = {0, 0, 0, 0};
+#pragma unroll 8
+    for (int s = 0; s < n; ++s) {
+      const float ms_ = __shfl(ms, s, 32), fs = __shfl(f, s, 32);
+      if (ms_ != -INFINITY) v += fs * *(const float4v*)(op + (int64_t)s * c.dim);
+    }
+    if (in) {
+      const int h = (int)(bh - (int64_t)row * a.n_heads);
+      typedef T x4 __attribute__((ext_vector_type(4)));
+      x4 y;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) y[k] = (T)(l == 0.0f ? 0.0f : v[k] / l);
+      *(x4*)((T*)a.out + (int64_t)row * a.ldo + h * c.dim + e) = y;
+    }
+    if (lse && lane == 0) lse[bh] = l == 0.0f ? INFINITY : m + log2f(l);
+  }
+}
+
+// The same after the one-token kernel: the first n_seqs n_heads blocks the outputs, the
+// others the weights of kJoinSteps steps of one key head.
 constexpr int kJoinSteps = 32;
 
 template <typename T>
@@ -440,29 +531,7 @@ __global__ __launch_bounds__(256) void token_join_kernel(KvView c, KvAttnArgs a,
   extern __shared__ float sh[];
   const int tid = threadIdx.x;
   if ((int)blockIdx.x < c.n_seqs * a.n_heads) {
-    const int64_t bh = blockIdx.x;
-    const float* ml = w.ml + bh * w.n_splits * 2;
-    float m, l;
-    join_ml(ml, w.n_splits, &m, &l);
-    const int g = tid >> 5, e = (tid & 31) * 4;
-    const bool in = e < c.dim;
-    const float* o = w.o + bh * w.n_splits * c.dim + (in ? e : 0);
-    float4v v = {0, 0, 0, 0};
-#pragma unroll 4
-    for (int s = g; s < w.n_splits; s += 8)
-      v += __builtin_amdgcn_exp2f(ml[2 * s] - m) * *(const float4v*)(o + (int64_t)s * c.dim);
-    *(float4v*)(sh + 4 * tid) = v;
-    __syncthreads();
-    if (g == 0 && in) {
-#pragma unroll
-      for (int k = 1; k < 8; ++k) v += *(const float4v*)(sh + 4 * (tid + 32 * k));
-      const int b = bh / a.n_heads, h = bh - (int64_t)b * a.n_heads;
-      typedef T x4 __attribute__((ext_vector_type(4)));
-      x4 y;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) y[k] = (T)(l == 0.0f ? 0.0f : v[k] / l);
-      *(x4*)((T*)a.out + (int64_t)b * a.ldo + (int64_t)h * c.dim + e) = y;
-    }
+    join_row<T>(c, a, w.parts, blockIdx.x, nullptr, sh);
     return;
   }
   const int group = a.n_heads / c.n_kv;
@@ -477,7 +546,7 @@ __global__ __launch_bounds__(256) void token_join_kernel(KvView c, KvAttnArgs a,
   const int64_t bh0 = (int64_t)b * a.n_heads + kvh * group;
   for (int h = tid >> 6; h < group; h += 4) {
     float m, l;
-    join_ml(w.ml + (bh0 + h) * w.n_splits * 2, w.n_splits, &m, &l);
+    join_ml(w.parts.ml + (bh0 + h) * w.parts.n_splits * 2, w.parts.n_splits, &m, &l);
     if ((tid & 63) == 0) {
       sh[2 * h] = m;
       sh[2 * h + 1] = l == 0.0f ? 0.0f : 1.0f / l;
@@ -514,8 +583,8 @@ int64_t splits_of(const KvView& c, int64_t n_heads, int64_t window, int64_t sink
 
 TokenWs layout(const KvView& c, int64_t n_heads, int64_t window, int64_t sinks, bool weights, void* ws, size_t* bytes) {
   TokenWs w{};
-  w.n_splits = (int)splits_of(c, n_heads, window, sinks);
-  w.join = w.n_splits > 1 || (weights && n_heads / c.n_kv > 16);
+  w.parts.n_splits = (int)splits_of(c, n_heads, window, sinks);
+  w.join = w.parts.n_splits > 1 || (weights && n_heads / c.n_kv > 16);
   w.n_scores = (int)(max_steps(c, window, sinks) * kTile);
   const int64_t rows = (int64_t)c.n_seqs * n_heads;
   float* f = (float*)ws;
@@ -524,10 +593,10 @@ TokenWs layout(const KvView& c, int64_t n_heads, int64_t window, int64_t sinks, 
   w.scores = f;  // multiples of 4 floats each: all 16-byte aligned
   if (weights && !w.lds) n += (size_t)rows * w.n_scores;
   if (w.join) {
-    w.o = f + n;
-    n += (size_t)rows * w.n_splits * c.dim;
-    w.ml = f + n;
-    n += (size_t)rows * w.n_splits * 2;
+    w.parts.o = f + n;
+    n += (size_t)rows * w.parts.n_splits * c.dim;
+    w.parts.ml = f + n;
+    n += (size_t)rows * w.parts.n_splits * 2;
   }
   if (bytes) *bytes = n * sizeof(float);
   return w;
@@ -536,7 +605,7 @@ TokenWs layout(const KvView& c, int64_t n_heads, int64_t window, int64_t sinks, 
 template <typename T, int KS, int VEC>
 gptq_status_t launch(const KvView& c, const KvAttnArgs& a, const TokenWs& w, hipStream_t st) {
   const int64_t group = a.n_heads / c.n_kv;
-  const int64_t blocks = (int64_t)c.n_seqs * c.n_kv * ceil_div(group, 16) * w.n_splits;
+  const int64_t blocks = (int64_t)c.n_seqs * c.n_kv * ceil_div(group, 16) * w.parts.n_splits;
   if (blocks * 64 * NW >= (int64_t)1 << 32) return GPTQ_ERR_UNSUPPORTED;
   const dim3 grid((unsigned)blocks), blk(64 * NW);
   const size_t lds = NW * (size_t)std::min<int64_t>(group, 16) * (16 * VEC + 4) * sizeof(float);
@@ -577,6 +646,25 @@ size_t kv_token_workspace_bytes(const KvView& c, int64_t n_heads, int64_t window
   size_t bytes = 0;
   layout(c, n_heads, window, sinks, weights, nullptr, &bytes);
   return bytes;
+}
+
+template <typename T>
+static gptq_status_t join_enqueue(const KvView& c, const KvAttnArgs& a, const SplitWs& w, int64_t n_rows,
+                                  const int32_t* cu, float* lse, hipStream_t st) {
+  const bool few = w.n_splits <= kJoinFew;
+  const int64_t blocks = few ? ceil_div(n_rows * a.n_heads, 8) : n_rows * a.n_heads;
+  if (blocks * 256 >= (int64_t)1 << 32) return GPTQ_ERR_UNSUPPORTED;
+  if (few)
+    hipLaunchKernelGGL((join_rows_kernel<T, true>), dim3((unsigned)blocks), dim3(256), 0, st, c, a, w, cu, (int)n_rows, lse);
+  else
+    hipLaunchKernelGGL((join_rows_kernel<T, false>), dim3((unsigned)blocks), dim3(256), 0, st, c, a, w, cu, (int)n_rows, lse);
+  GPTQ_CHECK_LAUNCH();
+  return GPTQ_OK;
+}
+
+gptq_status_t kv_join_enqueue(const KvView& c, const KvAttnArgs& a, const SplitWs& w, int64_t n_rows,
+                              const int32_t* cu, float* lse, hipStream_t st) {
+  return c.bf16 ? join_enqueue<bf16_t>(c, a, w, n_rows, cu, lse, st) : join_enqueue<half_t>(c, a, w, n_rows, cu, lse, st);
 }
 
 gptq_status_t kv_token_enqueue(const KvView& c, const KvAttnArgs& a, void* ws, hipStream_t st) {

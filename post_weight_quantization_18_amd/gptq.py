@@ -544,7 +544,7 @@ def _attend(fn, name, lib, q, k, v, page_table, lens, cu_seqlens, scale, window,
         nbytes = lib.gptq_kv_workspace_bytes(cache, seqs, heads, window, sinks, 0, summed)
     else:
         rows = (_cu(cu_seqlens, seqs.n_seqs), n)
-        nbytes = lib.gptq_kv_workspace_bytes(cache, seqs, heads, window, sinks, n, summed) if summed else 0
+        nbytes = lib.gptq_kv_workspace_bytes(cache, seqs, heads, window, sinks, n, summed) if n else 0
     ws = None
     if nbytes:
         workspace = _workspace(nbytes, q.device, workspace)

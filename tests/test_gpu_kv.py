@@ -172,6 +172,55 @@ def test_prompts(case, weights):
         _near(wd, total, wtol + R.U * np.abs(total) * (added > 0), "weights")
 
 
+SPLIT = [
+    # dtype, lens, new, heads, kv, dim, page size, window, sinks, max_pages: few queries over many slots, whose tiles
+    # are split over blocks
+    ("fp16", [1111], [3], 2, 2, 128, 16, 0, 0, None),
+    ("bf16", [1300, 0, 9, 700], [150, 0, 9, 1], 4, 2, 64, 8, 0, 0, None),
+    ("fp16", [2100, 5], [40, 5], 3, 1, 80, 64, 900, 70, None),
+    ("bf16", [1999], [1], 7, 1, 40, 32, 700, 3, 100),
+    ("fp16", [64, 1], [64, 1], 2, 1, 96, 64, 0, 0, 40),  # the later splits have nothing
+]
+
+
+@pytest.mark.parametrize("weights", [False, True])
+@pytest.mark.parametrize("case", SPLIT, ids=lambda c: "-".join(map(str, c)).replace(" ", ""))
+def test_few_queries_over_many_slots(case, weights):
+    dtype, lens, new, heads, kv, dim, ps, window, sinks, max_pages = case
+    print(f"[case] split prompt {case} weights={weights}", flush=True)
+    c = Case(dtype, lens, heads, kv, dim, ps, max_pages=max_pages)
+    c.table[0, 0] = -1
+    cu = [0]
+    for x in new:
+        cu.append(cu[-1] + x)
+    q = c.queries(cu[-1] + 3)
+    k, v, table, ln = c.gpu()
+    w = c.weights()
+    wd = w.to(DEV) if weights else None
+    out = torch.full_like(q, 7.0).to(DEV)
+    assert G.kv_workspace_bytes(k, v, table, ln, heads, window=window, sinks=sinks, n_tokens=len(q)) > 0
+    G.paged_prefill(q.to(DEV), k, v, table, ln, torch.tensor(cu, dtype=torch.int32, device=DEV), window=window,
+                    sinks=sinks, weights=wd, out=out)
+    assert (out[cu[-1]:] == 7.0).all()
+    want, tol, added, wtol = c.expect(q[:cu[-1]], cu, window, sinks, HALF_STEP[dtype])
+    _near(out[:cu[-1]], want, tol, "out")
+    if weights:
+        total = w.double().numpy() + added
+        _near(wd, total, wtol + R.U * np.abs(total) * (added > 0), "weights")
+
+
+def test_split_rows_that_no_sequence_has_stay_as_they_were():
+    print("[case] split prompt, a sequence whose bounds leave the rows", flush=True)
+    c = Case("fp16", [800, 700], 2, 1, 64, 16)
+    q = c.queries(12)
+    k, v, table, ln = c.gpu()
+    out = torch.full_like(q, 7.0).to(DEV)
+    G.paged_prefill(q.to(DEV), k, v, table, ln, torch.tensor([0, 5, 40], dtype=torch.int32, device=DEV), out=out)
+    assert (out[5:] == 7.0).all()
+    want, tol, _, _ = c.expect(q[:5], [0, 5, 5], 0, 0, 2.0 ** -11)
+    _near(out[:5], want, tol, "out")
+
+
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 def test_prompt_rows_do_not_see_values_that_are_not_finite_behind_their_mask(dtype):
     """A NaN or infinite value reaches the rows that see its slot and no other."""
