@@ -343,8 +343,10 @@ gptq_status_t gptq_pack_codes(const uint8_t* codes, int64_t m, int64_t d, int32_
  *  lens     device int32 [n_seqs]: slots in use, the call's new tokens counted.
  *           Negative reads as 0, more than max_pages * page_size as that.
  * An entry outside [0, n_pages) holds no slots: attention passes over them (they
- * are in no softmax and get no weight), append and evict skip their rows. So
- * whatever the table holds, no access leaves the buffers.
+ * are in no softmax and get no weight), append and evict skip their rows (a slot
+ * on no page that an eviction keeps becomes a slot of a new page, whose row holds
+ * what it held before: evict sequences whose pages are all there). So whatever
+ * the table holds, no access leaves the buffers.
  * Lengths, tables and offsets are read on the device when the kernels run: a
  * captured graph replays with the values they hold then. */
 typedef struct {
@@ -374,7 +376,7 @@ typedef struct {
  *           cu_seqlens[b + 1] - 1, ascending from 0; rows behind the last
  *           sequence are ignored. NULL: one row per sequence (n_tokens ==
  *           n_seqs). A sequence may have none.
- * Slots below 0 or beyond the table are skipped. Two sequences whose new slots
+ * n_tokens < 2^24. Slots below 0 or beyond the table are skipped. Two sequences whose new slots
  * share a page row leave one of the two there. */
 gptq_status_t gptq_kv_append(const gptq_kv_cache_t* cache, const gptq_kv_seqs_t* seqs, const void* k_new, int64_t ldk,
                              const void* v_new, int64_t ldv, const int32_t* cu_seqlens, int64_t n_tokens,
@@ -425,7 +427,7 @@ gptq_status_t gptq_paged_attention(const gptq_kv_cache_t* cache, const gptq_kv_s
  *           partial results, and any call with weights).
  * The weights enter the second product in the cache's type. The order of the sums
  * depends on the sizes given from the host (n_tokens, n_seqs, max_pages), not on
- * lens or timing. */
+ * the other sequences' lengths or on timing. */
 gptq_status_t gptq_paged_prefill(const gptq_kv_cache_t* cache, const gptq_kv_seqs_t* seqs, const void* q, int64_t ldq,
                                  const int32_t* cu_seqlens, int64_t n_tokens, int64_t n_heads, float scale,
                                  int64_t window, int64_t sinks, float* weights, int64_t ldw, void* out, int64_t ldo,

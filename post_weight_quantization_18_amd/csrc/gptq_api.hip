@@ -323,6 +323,7 @@ gptq_status_t gptq_kv_append(const gptq_kv_cache_t* cache, const gptq_kv_seqs_t*
   if (n_tokens == 0) return GPTQ_OK;
   if (!k_new || !v_new || ldk < row || ldv < row || ldk % 8 || ldv % 8) return GPTQ_ERR_INVALID_ARG;
   if (!aligned(k_new, 16) || !aligned(v_new, 16)) return GPTQ_ERR_INVALID_ARG;
+  if (n_tokens >= ((int64_t)1 << 24)) return GPTQ_ERR_UNSUPPORTED;  // one block's threads for each fit a grid
   GPTQ_CHECK_DEVICE();
   return kv_append_enqueue(c, k_new, ldk, v_new, ldv, cu_seqlens, n_tokens, (hipStream_t)stream);
 }

@@ -103,7 +103,7 @@ struct SplitWs {
   int n_splits;
 };
 // Joins them into those of the n_rows rows of out that a sequence of the ragged batch cu has;
-// lse (optional): log2 of the sum of 2^score per row and head.
+// lse [n_heads][n_rows] (optional): log2 of the sum of 2^score.
 gptq_status_t kv_join_enqueue(const KvView& c, const KvAttnArgs& a, const SplitWs& w, int64_t n_rows,
                               const int32_t* cu, float* lse, hipStream_t st);
 

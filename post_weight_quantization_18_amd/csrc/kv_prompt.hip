@@ -30,6 +30,7 @@ constexpr int kT = 64;      // slots per tile
 constexpr int kRing = 2;    // tiles in LDS
 constexpr int kLeast = 4;   // tiles per block where they are split
 constexpr int kW = 64;      // queries at a time in the weights' kernel
+constexpr int kWRing = 3;   // and how many of these are in LDS (the wait in front of a step counts on three)
 constexpr float kRaise = 8.0f;
 
 // The slots some query of a block sees, as tiles of kT.
@@ -149,6 +150,19 @@ __device__ __forceinline__ void dma16_from(const void* base, uint32_t off, uint3
       : "s"(lds), "v"(off), "s"(base)
       : "memory");
 }
+// The same, 4 bytes per lane.
+__device__ __forceinline__ void dma4_from(const void* base, uint32_t off, uint32_t lds) {
+  uint32_t saved;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %1\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dword %2, %3\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(saved)
+      : "s"(lds), "v"(off), "s"(base)
+      : "memory");
+}
 // Eight rows of K and of V in one go, N transfers each, 1 KB apart in LDS.
 template <int N>
 __device__ __forceinline__ void dma16_octet(const void* kb, const void* vb, const uint32_t (&ok)[N],
@@ -218,7 +232,7 @@ struct Ring {
 };
 
 // What a block leaves: its rows of out; with them the rows' log2 of the sum of 2^score in
-// lse [n_tokens][n_heads]; or, where a piece's tiles are split over n_splits blocks, the
+// lse [n_heads][n_tokens] (the weights' kernel reads 32 rows of one head at a time); or, where a piece's tiles are split over n_splits blocks, the
 // unnormalized sums with their maximum and weight in parts [n_tokens][n_heads][n_splits].
 constexpr int kOut = 0, kOutLse = 1, kParts = 2;
 
@@ -604,7 +618,7 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(KvView c, KvAttnArgs a, 
     if constexpr (MODE == kOutLse) {
       // a row without a weight: +infinity, so that 2^(score - lse) is 0
       if (half == 0)
-        lse[row * a.n_heads + h] = lsum == 0.0f ? INFINITY : (m == -INFINITY ? 0.0f : m * sc) + log2f(lsum);
+        lse[(int64_t)h * n_rows + row] = lsum == 0.0f ? INFINITY : (m == -INFINITY ? 0.0f : m * sc) + log2f(lsum);
     }
   }
 }
@@ -623,7 +637,8 @@ __global__ __launch_bounds__(256, 2) void prompt_weights_kernel(KvView c, KvAttn
   using x8 = typename KT::x8;
   using R = Ring<QS>;
   constexpr int kRows = 64 / R::kLpr, kDma = 16 / kRows, kBytes = kW * R::kPitch;
-  __shared__ __attribute__((aligned(1024))) char smem[2 * kBytes];
+  __shared__ __attribute__((aligned(1024))) char smem[kWRing * kBytes];
+  __shared__ float lse_of[4][kWRing][kW];  // of each wave's own transfer
   const GPTQ_LDS char* lds = (const GPTQ_LDS char*)smem;
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
   // the first slots, which most queries see, of all sequences and heads first
@@ -678,9 +693,10 @@ __global__ __launch_bounds__(256, 2) void prompt_weights_kernel(KvView c, KvAttn
   auto after = [&](At p) __attribute__((always_inline)) {
     return p.i + kW < i_hi ? At{p.hh, p.i + kW} : At{p.hh + 1, i_lo};
   };
-  auto stage = [&](int s, At p) __attribute__((always_inline)) {
+  // (always kDma + 1 transfers: no row is without its first chunks)
+  auto stage = [&](int buf, At p) __attribute__((always_inline)) {
     const int hh = p.hh, i0 = p.i + 16 * wave;
-    const uint32_t to = lds0 + (s & 1) * kBytes + 16 * wave * R::kPitch;
+    const uint32_t to = lds0 + buf * kBytes + 16 * wave * R::kPitch;
     const T* from = qb + uni((int64_t)(i0 < n_b ? i0 : n_b - 1) * a.ldq + (int64_t)hh * c.dim);
     const int left = i0 < n_b ? n_b - 1 - i0 : 0;  // last row that is there
 #pragma unroll
@@ -689,45 +705,73 @@ __global__ __launch_bounds__(256, 2) void prompt_weights_kernel(KvView c, KvAttn
       const uint32_t off = (uint32_t)((r < left ? r : left) * (uint32_t)a.ldq + (ch < chunks ? ch : 0) * 8) * 2;
       if (exact || ch < chunks) dma16_from(from, off, to + 1024 * i);
     }
+    const int i = p.i + lane < n_b ? p.i + lane : n_b - 1;
+    dma4_from(lse + uni((int64_t)(kvh * group + hh) * n_rows + r0), (uint32_t)i * 4,
+              (uint32_t)(uintptr_t)(const GPTQ_LDS char*)&lse_of[wave][buf][0]);
   };
-  auto row_lse = [&](At p, int u) __attribute__((always_inline)) {
-    const int i = p.i + 32 * u + col;
-    return lse[(int64_t)(r0 + (i < n_b ? i : n_b - 1)) * a.n_heads + kvh * group + p.hh];
-  };
-  const int qrow = col;
   uint32_t at_q[QS];
 #pragma unroll
-  for (int i = 0; i < QS; ++i) at_q[i] = qrow * R::kPitch + (((2 * i + half) ^ R::fk(qrow)) * 16);
+  for (int i = 0; i < QS; ++i) at_q[i] = col * R::kPitch + (((2 * i + half) ^ R::fk(col)) * 16);
+  struct Queries {
+    x8 f[QS];
+  };
+  auto queries = [&](const GPTQ_LDS char* buf, int u) __attribute__((always_inline)) {
+    Queries z;
+#pragma unroll
+    for (int i = 0; i < QS; ++i) z.f[i] = *(const GPTQ_LDS x8*)(buf + at_q[i] + 32 * u * R::kPitch);
+    return z;
+  };
+  auto scores = [&](const Queries& z) __attribute__((always_inline)) {
+    float16v x = (float16v){0};
+#pragma unroll
+    for (int i = 0; i < QS; ++i) x = KT::mfma32(k[i], z.f[i], x);
+    return x;
+  };
 
   if (total > 0) {
     if (!exact)
-      for (int i = tid; i < 2 * kBytes / 16; i += 256) *(GPTQ_LDS uint4v*)(lds + 16 * i) = (uint4v){0, 0, 0, 0};
+      for (int i = tid; i < kWRing * kBytes / 16; i += 256) *(GPTQ_LDS uint4v*)(lds + 16 * i) = (uint4v){0, 0, 0, 0};
     __syncthreads();
-    At now = {0, i_lo};
-    stage(0, now);
-    float l0 = row_lse(now, 0), l1 = row_lse(now, 1);
+    At now = {0, i_lo}, ahead = now;  // the queries used, and those transferred
+    int cur = 0, to = 0;              // and their buffers
+    for (int s = 0; s < kWRing - 1 && s < total; ++s) {
+      stage(to++, ahead);
+      ahead = after(ahead);
+    }
     for (int s = 0; s < total; ++s) {
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-      lds_barrier();
-      const At next = s + 1 < total ? after(now) : now;
-      if (s + 1 < total) stage(s + 1, next);
-      const float n0 = row_lse(next, 0), n1 = row_lse(next, 1);
-      const GPTQ_LDS char* buf = lds + (s & 1) * kBytes;
-      const int i0 = now.i;
-      now = next;
+      // this wave's rows of step s have landed; those of the next step may be under way
+      if (s + 1 < total)
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((kWRing - 2) * (kDma + 1)) : "memory");
+      else
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      lds_barrier();  // for every wave, and step s - 1 is read by none
+      if (s + kWRing - 1 < total) {
+        stage(to, ahead);
+        ahead = after(ahead);
+      }
+      to = to + 1 < kWRing ? to + 1 : 0;
+      const GPTQ_LDS char* buf = lds + cur * kBytes;
+      const float l0 = lse_of[wave][cur][col], l1 = lse_of[wave][cur][32 + col];
+      cur = cur + 1 < kWRing ? cur + 1 : 0;
+      const int i0 = now.i, lowest = base + i0;
+      now = after(now);
+      if (t0 + 31 <= lowest && i0 + kW <= n_b &&
+          (a.window <= 0 || t0 > lowest + kW - 1 - a.window || t0 + 32 <= a.sinks)) {
+        // every query sees all of this wave's slots: one straight piece of code
+        const Queries z0 = queries(buf, 0), z1 = queries(buf, 1);
+        __builtin_amdgcn_sched_barrier(0);
+        const float16v x = scores(z0), y = scores(z1);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        float16v x = (float16v){0};
+        for (int r = 0; r < 16; ++r) acc[r] += __builtin_amdgcn_exp2f(fmaf(x[r], sc, -l0));
 #pragma unroll
-        for (int i = 0; i < QS; ++i) x = KT::mfma32(k[i], *(const GPTQ_LDS x8*)(buf + at_q[i] + 32 * u * R::kPitch), x);
-        const float l = u ? l1 : l0;
-        const int lowest = base + i0 + 32 * u;
-        if (t0 + 31 <= lowest && i0 + 32 * u + 32 <= n_b &&
-            (a.window <= 0 || t0 > lowest + 31 - a.window || t0 + 32 <= a.sinks)) {
-#pragma unroll
-          for (int r = 0; r < 16; ++r) acc[r] += __builtin_amdgcn_exp2f(fmaf(x[r], sc, -l));
-        } else {
-          const int pos = lowest + col;
+        for (int r = 0; r < 16; ++r) acc[r] += __builtin_amdgcn_exp2f(fmaf(y[r], sc, -l1));
+      } else {
+        for (int u = 0; u < 2; ++u) {
+          const int low = lowest + 32 * u;  // position of the first of 32 queries
+          if (low + 31 < t0 || (a.window > 0 && t0 + 31 <= low - a.window && t0 >= a.sinks)) continue;  // none sees any
+          const float16v x = scores(queries(buf, u));
+          const float l = u ? l1 : l0;
+          const int pos = low + col;
           uint32_t see = low_bits(pos + 1 - t0);
           if (a.window > 0) see &= ~low_bits(pos + 1 - a.window - t0) | low_bits(a.sinks - t0);
           if (i0 + 32 * u + col >= n_b) see = 0;
@@ -739,21 +783,23 @@ __global__ __launch_bounds__(256, 2) void prompt_weights_kernel(KvView c, KvAttn
           }
         }
       }
-      l0 = n0;
-      l1 = n1;
     }
   }
+  // Sums along the rows: at every step a lane passes on half of the sums it holds, so that
+  // lanes 2 r and 2 r + 1 (of each half) end up with row r's, and one lane reads and writes each
+  // weight.
 #pragma unroll
-  for (int r = 0; r < 16; ++r)
-    for (int o = 16; o > 0; o >>= 1) acc[r] += __shfl_xor(acc[r], o);
-  if (col == 0) {
-    float* wt = a.weights + ((int64_t)b * c.n_kv + kvh) * a.ldw;
+  for (int n = 8, o = 16; n > 0; n >>= 1, o >>= 1)
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int t = t0 + 16 * (r >> 3) + 8 * half + (r & 7);
-      if (t < len && c.page_ok(table[t >> c.page_shift])) wt[t] += acc[r];
+    for (int i = 0; i < n; ++i) {
+      const float lo = acc[i], hi = acc[i + n];
+      const bool up = col & o;
+      acc[i] = (up ? hi : lo) + __shfl_xor(up ? lo : hi, o);
     }
-  }
+  const float sum = acc[0] + __shfl_xor(acc[0], 1);
+  const int r = col >> 1, t = t0 + 16 * (r >> 3) + 8 * half + (r & 7);
+  if ((col & 1) == 0 && t < len && c.page_ok(table[t >> c.page_shift]))
+    a.weights[((int64_t)b * c.n_kv + kvh) * a.ldw + t] += sum;
 }
 
 int64_t pieces_of(const KvView& c, int64_t n_tokens, int64_t n_heads) {

@@ -458,7 +458,7 @@ __device__ __forceinline__ void join_row(const KvView& c, const KvAttnArgs& a, c
     for (int k = 0; k < 4; ++k) y[k] = (T)(l == 0.0f ? 0.0f : v[k] / l);
     *(x4*)((T*)a.out + row * a.ldo + h * c.dim + e) = y;
   }
-  if (lse && tid == 0) lse[bh] = l == 0.0f ? INFINITY : m + log2f(l);
+  if (lse && tid == 0) *lse = l == 0.0f ? INFINITY : m + log2f(l);
 }
 
 // Row and head bh belong to a sequence of the ragged batch (rows behind the last one, say, stay
@@ -484,7 +484,8 @@ __global__ __launch_bounds__(256) void join_rows_kernel(KvView c, KvAttnArgs a, 
   if constexpr (!FEW) {
     __shared__ float sh[1024];
     if (__syncthreads_or(owned(c, cu, n_rows, blockIdx.x / a.n_heads, threadIdx.x, 256)))
-      join_row<T>(c, a, w, blockIdx.x, lse, sh);
+      join_row<T>(c, a, w, blockIdx.x, lse ? lse + (int64_t)(blockIdx.x % a.n_heads) * n_rows + blockIdx.x / a.n_heads : lse,
+                  sh);
   } else {
     const int64_t bh = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31, row = (int)(bh / a.n_heads), n = w.n_splits;
@@ -510,15 +511,15 @@ __global__ __launch_bounds__(256) void join_rows_kernel(KvView c, KvAttnArgs a, 
       const float ms_ = __shfl(ms, s, 32), fs = __shfl(f, s, 32);
       if (ms_ != -INFINITY) v += fs * *(const float4v*)(op + (int64_t)s * c.dim);
     }
+    const int h = (int)(bh - (int64_t)row * a.n_heads);
     if (in) {
-      const int h = (int)(bh - (int64_t)row * a.n_heads);
       typedef T x4 __attribute__((ext_vector_type(4)));
       x4 y;
 #pragma unroll
       for (int k = 0; k < 4; ++k) y[k] = (T)(l == 0.0f ? 0.0f : v[k] / l);
       *(x4*)((T*)a.out + (int64_t)row * a.ldo + h * c.dim + e) = y;
     }
-    if (lse && lane == 0) lse[bh] = l == 0.0f ? INFINITY : m + log2f(l);
+    if (lse && lane == 0) lse[(int64_t)h * n_rows + row] = l == 0.0f ? INFINITY : m + log2f(l);
   }
 }
 

@@ -210,9 +210,10 @@ class GenerationBlock:
 
     prompt(x, lens)   the first tokens of every sequence (or more of them)
     token(x)          one token of every sequence
-    With budget > 0 the attention weights of every slot are accumulated, and once a
-    sequence holds more than budget + slack slots it falls back to budget: its first
-    `sinks`, its last `recent` and the most attended others stay. With window > 0
+    With budget > 0 the attention weights of every slot are accumulated, and once some
+    sequence holds more than budget + slack slots, all that hold more than budget fall
+    back to it: their first `sinks`, their last `recent` and the most attended others
+    stay. With window > 0
     a token sees the last `window` slots and the first `sinks`.
     Pages are taken from a free list as sequences grow, and given back by eviction."""
 
@@ -239,6 +240,8 @@ class GenerationBlock:
 
     def _grow(self, new):
         """Room for new[b] more slots of every sequence; returns lens on the device."""
+        if len(new) != self.n_seqs or min(new) < 0:
+            raise ValueError(f"a count of new tokens for each of the {self.n_seqs} sequences, none negative")
         for b, n in enumerate(new):
             if self.lens[b] + n > self.max_pages * self.page_size:
                 raise ValueError(f"sequence {b} outgrows the cache ({self.lens[b]} + {n} slots)")
@@ -250,6 +253,10 @@ class GenerationBlock:
                 self.pages[b] += more
                 self.table[b, have:need] = torch.tensor(more, dtype=torch.int32, device=self.device)
         return torch.tensor(self.lens, dtype=torch.int32, device=self.device)
+
+    def _rows(self, x, n):
+        if x.dtype != torch.float16 or x.shape != (n, self.shape.d_model) or n == 0:
+            raise ValueError(f"x must be fp16 [{n}, {self.shape.d_model}], with a row at least")
 
     def _heads(self, t):
         return t.view(t.shape[0], self.shape.n_heads, self.head_dim)
@@ -266,6 +273,8 @@ class GenerationBlock:
         def product(name, t):
             return linear(t, self.results[name]["w_hat"])
 
+        lens = list(lens)
+        self._rows(x, sum(lens))
         dev_lens = self._grow(lens)
         cu = torch.tensor([0, *lens], dtype=torch.int32).cumsum(0, dtype=torch.int32).to(self.device)
         a = layer_norm(x)
@@ -284,6 +293,7 @@ class GenerationBlock:
             return torch.stack([G.dequant_gemv(r["qcodes"], r["scales"], r["zeros"], bits, group, row) for row in
                                 t.contiguous()]).half()
 
+        self._rows(x, self.n_seqs)
         dev_lens = self._grow([1] * self.n_seqs)
         a = layer_norm(x)
         q, k, v = (self._heads(product(n, a)) for n in ("q", "k", "v"))

@@ -136,4 +136,8 @@ def test_a_sequence_that_outgrows_its_cache_is_refused(results):
     x = torch.zeros(33, SHAPE.d_model, dtype=torch.float16, device=DEV)
     with pytest.raises(ValueError, match="outgrows"):
         block.prompt(x, [33])
+    for call in (lambda: block.prompt(x, [32]), lambda: block.prompt(x, [33, 0]), lambda: block.prompt(x[:5], [-1, 6]),
+                 lambda: block.prompt(x[:0], [0]), lambda: block.token(x), lambda: block.token(x[:1].float())):
+        with pytest.raises(ValueError):
+            call()
     assert block.lens == [0] and len(block.free) == 2

@@ -100,6 +100,7 @@ TOKEN = [
     ("fp16", [9000], 256, 256, 8, 256, 0, 0),          # whole, scores too many for LDS
     ("fp16", [500, 3], 32, 2, 128, 16, 0, 0),          # 16 heads a key: all the LDS that the scores may take
     ("bf16", [2100, 40, 0], 34, 2, 64, 32, 1500, 3),   # 17 heads a key, splits and a window
+    ("fp16", [i % 7 for i in range(70)] + [90], 2, 2, 16, 8, 0, 0),
 ]
 
 
@@ -145,6 +146,7 @@ PROMPT = [
     ("bf16", [1500, 700], [300, 2], 2, 2, 64, 64, 700, 5),
     ("fp16", [600, 580], [600, 580], 1, 1, 80, 8, 64, 100),
     ("fp16", [3, 20], [10, 25], 2, 2, 64, 8, 0, 0),     # more new tokens than slots: rows that see nothing
+    ("bf16", [i % 9 for i in range(70)] + [300, 2], [i % 9 for i in range(70)] + [260, 1], 1, 1, 16, 8, 0, 0),
 ]
 
 
@@ -180,6 +182,7 @@ SPLIT = [
     ("fp16", [2100, 5], [40, 5], 3, 1, 80, 64, 900, 70, None),
     ("bf16", [1999], [1], 7, 1, 40, 32, 700, 3, 100),
     ("fp16", [64, 1], [64, 1], 2, 1, 96, 64, 0, 0, 40),  # the later splits have nothing
+    ("fp16", [700] + [i % 5 for i in range(129)], [40] + [min(1, i % 5) for i in range(129)], 1, 1, 8, 8, 0, 0, 200),
 ]
 
 

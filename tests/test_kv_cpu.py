@@ -69,6 +69,7 @@ def test_append_refusals(lib):
     assert call(k_new=P + 8) == BAD
     assert call(n=4) == BAD                    # one row per sequence without cu_seqlens
     assert call(n=-1, cu=P) == BAD and call(n=1 << 30, cu=P) == BAD
+    assert call(n=1 << 24, cu=P) == UNSUP
     assert call(n=0, cu=P, k_new=None, v_new=None) == G.GPTQ_OK
 
 
