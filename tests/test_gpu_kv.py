@@ -566,6 +566,40 @@ def test_captured_prompt_and_eviction():
             assert torch.equal(a, b)
 
 
+def test_captured_split_chunks_replay_with_the_lengths_of_the_moment():
+    print("[case] graph of a chunk whose tiles are split", flush=True)
+    c = Case("fp16", [1500, 900], 4, 2, 64, 16)
+    q = c.queries(60).to(DEV)
+    k, v, table, ln = c.gpu()
+    cu = torch.tensor([0, 40, 60], dtype=torch.int32, device=DEV)
+    w, out = torch.zeros(2, 2, table.shape[1] * 16, device=DEV), torch.empty_like(q)
+    assert G.kv_workspace_bytes(k, v, table, ln, 4, n_tokens=60) > 0
+
+    def run():
+        w.zero_()
+        out.fill_(7.0)
+        G.paged_prefill(q, k, v, table, ln, cu, weights=w, out=out)
+
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for lens, rows in (([1500, 900], [0, 40, 60]), ([1200, 17], [0, 57, 60]), ([64, 900], [0, 0, 33]), ([5, 0], [0, 5, 5]),
+                       ([1500, 900], [0, 40, 60])):
+        ln.copy_(torch.tensor(lens, dtype=torch.int32))
+        cu.copy_(torch.tensor(rows, dtype=torch.int32))
+        run()
+        want = out.clone(), w.clone()
+        w.fill_(3.0)
+        out.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(w, want[1])
+        assert (out[rows[-1]:] == 7.0).all()
+
+
 def test_calls_on_two_streams_at_once():
     """Two batches on two streams, each with its own workspace, give what each gives alone."""
     print("[case] two streams", flush=True)
