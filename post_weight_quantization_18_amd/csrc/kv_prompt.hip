@@ -242,8 +242,9 @@ struct Ring {
 };
 
 // What a block leaves: its rows of out; with them the rows' log2 of the sum of 2^score in
-// lse [n_heads][n_tokens] (the weights' kernel reads 32 rows of one head at a time); or, where a piece's tiles are split over n_splits blocks, the
-// unnormalized sums with their maximum and weight in parts [n_tokens][n_heads][n_splits].
+// lse [n_heads][n_tokens] (the weights' kernel reads 64 rows of one head at a time); or, where
+// a piece's tiles are split over n_splits blocks, the unnormalized sums with their maximum and
+// weight in parts [n_tokens][n_heads][n_splits].
 constexpr int kOut = 0, kOutLse = 1, kParts = 2;
 
 // QS: steps of 16 along the head for the scores (16 QS >= dim).
@@ -429,7 +430,8 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(KvView c, KvAttnArgs a, 
     const int j = lane & 15, r = 8 * half + (j >> 2);
 #pragma unroll
     for (int i = 0; i < NO; ++i)
-      at_v[i] = R::kHalf + r * R::kPitch + (((4 * i + 2 * ((lane >> 4) & 1) + ((j & 3) >> 1)) ^ R::fv(r)) * 16) + 8 * (j & 1);
+      at_v[i] =
+          R::kHalf + r * R::kPitch + (((4 * i + 2 * ((lane >> 4) & 1) + ((j & 3) >> 1)) ^ R::fv(r)) * 16) + 8 * (j & 1);
   }
   // Operands are read from LDS well before the products that take them: a read takes longer
   // than a product, and left to itself the compiler waits for each in turn.
@@ -603,7 +605,8 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(KvView c, KvAttnArgs a, 
 #pragma unroll
         for (int r4 = 0; r4 < 4; ++r4) {
           const int e = 32 * i + 8 * r4 + 4 * half;
-          if (s0 < s1 && e < dim) *(float4v*)(pp + e) = (float4v){o[i][4 * r4], o[i][4 * r4 + 1], o[i][4 * r4 + 2], o[i][4 * r4 + 3]};
+          if (s0 < s1 && e < dim)
+            *(float4v*)(pp + e) = (float4v){o[i][4 * r4], o[i][4 * r4 + 1], o[i][4 * r4 + 2], o[i][4 * r4 + 3]};
         }
       if (half == 0) {
         parts.ml[2 * part] = m == -INFINITY ? -INFINITY : m * sc;
@@ -638,7 +641,7 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(KvView c, KvAttnArgs a, 
 // as S^T tiles whose rows, the slots, are summed along. One block owns 128 slots
 // of one key head (a wave 32, its keys in registers) and goes over all queries
 // that may see them, 64 at a time through LDS (DMA, the next 64 while these are
-// used; a third buffer costs a block of the four on a compute unit and 5 us of 57), so
+// used; a third buffer costs one of the four blocks on a compute unit: 61 us instead of 57), so
 // every sum has one owner and one order. Bound by the vector unit, which is busy 70 % of
 // the time: per score an exponential (16 cycles a wave), a multiply-add and a sum,
 // against 2 QS cycles of products. Six OPT-2.7B prompts of 65 to 1999 tokens, 32
@@ -746,7 +749,8 @@ __global__ __launch_bounds__(256, 2) void prompt_weights_kernel(KvView c, KvAttn
   const float old = *wt;
   x8 k[QS];
   {
-    const T* kp = (const T*)c.k + (c.page_ok(pg) ? c.head_base(pg, kvh) + (int64_t)(tk & (c.page_size - 1)) * c.dim : 0);
+    const T* kp =
+        (const T*)c.k + (c.page_ok(pg) ? c.head_base(pg, kvh) + (int64_t)(tk & (c.page_size - 1)) * c.dim : 0);
 #pragma unroll
     for (int i = 0; i < QS; ++i) {
       const int ch = 2 * i + half;

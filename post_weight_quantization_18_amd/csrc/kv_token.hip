@@ -477,9 +477,9 @@ __device__ __forceinline__ bool owned(const KvView& c, const int32_t* cu, int n_
 }
 
 // Joins the splits of all rows of a ragged batch, bound by reading them: many splits of few rows
-// with a block for each row and head; of up to 16 each thread of half a wave goes through all
-// (512 rows of 32 heads, 3 splits: a block each takes 25 us with the attention's 29, half a
-// wave 10).
+// with a block for each row and head; up to 16 of them (as many lanes hold their maxima) by half
+// a wave, which goes through all. 512 queries, 32 heads of 128, 712 slots in 3 splits: the call
+// takes 48 us with a block each, 28 with half a wave.
 constexpr int kJoinFew = 16;
 
 template <typename T, bool FEW>
@@ -488,8 +488,8 @@ __global__ __launch_bounds__(256) void join_rows_kernel(KvView c, KvAttnArgs a, 
   if constexpr (!FEW) {
     __shared__ float sh[1024];
     if (__syncthreads_or(owned(c, cu, n_rows, blockIdx.x / a.n_heads, threadIdx.x, 256)))
-      join_row<T>(c, a, w, blockIdx.x, lse ? lse + (int64_t)(blockIdx.x % a.n_heads) * n_rows + blockIdx.x / a.n_heads : lse,
-                  sh);
+      join_row<T>(c, a, w, blockIdx.x,
+                  lse ? lse + (int64_t)(blockIdx.x % a.n_heads) * n_rows + blockIdx.x / a.n_heads : nullptr, sh);
   } else {
     const int64_t bh = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31, row = (int)(bh / a.n_heads), n = w.n_splits;
@@ -660,16 +660,19 @@ static gptq_status_t join_enqueue(const KvView& c, const KvAttnArgs& a, const Sp
   const int64_t blocks = few ? ceil_div(n_rows * a.n_heads, 8) : n_rows * a.n_heads;
   if (blocks * 256 >= (int64_t)1 << 32) return GPTQ_ERR_UNSUPPORTED;
   if (few)
-    hipLaunchKernelGGL((join_rows_kernel<T, true>), dim3((unsigned)blocks), dim3(256), 0, st, c, a, w, cu, (int)n_rows, lse);
+    hipLaunchKernelGGL((join_rows_kernel<T, true>), dim3((unsigned)blocks), dim3(256), 0, st, c, a, w, cu, (int)n_rows,
+                       lse);
   else
-    hipLaunchKernelGGL((join_rows_kernel<T, false>), dim3((unsigned)blocks), dim3(256), 0, st, c, a, w, cu, (int)n_rows, lse);
+    hipLaunchKernelGGL((join_rows_kernel<T, false>), dim3((unsigned)blocks), dim3(256), 0, st, c, a, w, cu, (int)n_rows,
+                       lse);
   GPTQ_CHECK_LAUNCH();
   return GPTQ_OK;
 }
 
 gptq_status_t kv_join_enqueue(const KvView& c, const KvAttnArgs& a, const SplitWs& w, int64_t n_rows,
                               const int32_t* cu, float* lse, hipStream_t st) {
-  return c.bf16 ? join_enqueue<bf16_t>(c, a, w, n_rows, cu, lse, st) : join_enqueue<half_t>(c, a, w, n_rows, cu, lse, st);
+  return c.bf16 ? join_enqueue<bf16_t>(c, a, w, n_rows, cu, lse, st)
+                : join_enqueue<half_t>(c, a, w, n_rows, cu, lse, st);
 }
 
 gptq_status_t kv_token_enqueue(const KvView& c, const KvAttnArgs& a, void* ws, hipStream_t st) {
